@@ -421,6 +421,132 @@ MUON_API muon_status_t muon_entropy_profile(muon_entropy_plan_t plan, int32_t en
 /* Waits for the plan's last stream and frees it; NULL is ignored. */
 MUON_API void muon_entropy_destroy(muon_entropy_plan_t plan);
 
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit matrices: the 4-bit copies of weights, activations and
+ * output gradients that a model's products read, next to the fp32 masters
+ * that muon_step updates.
+ *
+ * A matrix [rows, k] holds each value as an e2m1 code (0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6 and a sign) times the scale of its block of consecutive k:
+ *   MUON_FP4_MX  blocks of 32, scale 2^(floor(log2 amax_block) - 2) held as
+ *                e8m0 (the exponent plus 127, at least 0);
+ *   MUON_FP4_NV  blocks of 16, scale s g: s = amax_block / (6 g) rounded to
+ *                e4m3, g the matrix's power of two, the least (and at least
+ *                2^-100) with amax_matrix <= 2688 g.
+ * Every rounding is to nearest, ties to even, of the exact quotient; codes
+ * saturate at 6 and keep the sign of a zero.  A block with a NaN or an infinity gets a NaN scale (all its
+ * values read as NaN; amax_matrix is that of the finite values); a block of
+ * zeros, and an NV block whose s rounds to 0, reads as zeros.  An NV value
+ * within a factor 1.04 of fp32's largest may read as infinity.
+ *
+ * Storage (device memory; muon_fp4_sizes gives the bytes):
+ *   data    [rows, pitch] bytes, two codes a byte with the lower k in bits
+ *           0..3, pitch = 16 ceil(k / 32), 16-byte aligned; the codes past k
+ *           are 0.
+ *   scales  one byte a block, in atoms of 512 bytes, one atom for 128 rows x 4
+ *           blocks, the atoms in row-major order [ceil(rows / 128)]
+ *           [ceil(k / (4 block))], 16-byte aligned: row r, block b is byte
+ *           (r % 32) 16 + (r % 128 / 32) 4 + b % 4 of atom (r / 128, b / 4).
+ *           Bytes of no row or block are 0.
+ *   tensor_scale  NV: two floats, g and amax_matrix.  The products take any
+ *           finite g (a checkpoint's tensor scale need not be a power of two).
+ * ------------------------------------------------------------------------ */
+typedef enum { MUON_FP4_NONE = -1, MUON_FP4_MX = 0, MUON_FP4_NV = 1 } muon_fp4_format_t;
+
+typedef struct {
+  void*   data;          /* codes                                                     */
+  void*   scales;        /* scale bytes                                               */
+  float*  tensor_scale;  /* NV: {g, amax}; MX: ignored                                */
+  int64_t rows;          /* 0 <= rows <= 2^30                                         */
+  int64_t k;             /* 0 <= k <= 2^30                                            */
+  int32_t format;        /* muon_fp4_format_t                                         */
+  int32_t reserved;      /* must be 0                                                 */
+} muon_fp4_matrix_t;
+
+/* A source [rows, cols] and the 4-bit matrices to make of it: along its
+ * columns (blocks within a row: a matrix [rows, cols]), along its rows (blocks
+ * down a column: the transpose, a matrix [cols, rows]), or both from one read;
+ * a form that is not wanted has format MUON_FP4_NONE. */
+typedef struct {
+  const void* src;       /* [rows, cols], row i at src + i ld                          */
+  int64_t ld;            /* elements, >= cols                                          */
+  int64_t rows, cols;    /* 0 <= rows, cols <= 2^30                                    */
+  int32_t src_dtype;     /* muon_dtype_t                                               */
+  int32_t reserved;      /* must be 0                                                  */
+  muon_fp4_matrix_t along_cols;
+  muon_fp4_matrix_t along_rows;
+  void*   values_cols;   /* plans with values: [rows, cols] and [cols, rows] dense,    */
+  void*   values_rows;   /*   for muon_fp4_values (NULL otherwise)                     */
+} muon_fp4_source_t;
+
+/* Bytes of a 4-bit matrix, and the pitch of its codes (each output may be
+ * NULL).  Errors: INVALID_ARG. */
+MUON_API muon_status_t muon_fp4_sizes(int32_t format, int64_t rows, int64_t k, int64_t* pitch, size_t* data_bytes,
+                                      size_t* scale_bytes);
+
+/* Quantise one matrix, asynchronously on `stream`.  Both forms have one
+ * format.  An empty source is a no-op.  No output may overlap the source or
+ * another output.  Deterministic: every output bit is fixed by the source.
+ * Errors: INVALID_ARG, SHAPE_MISMATCH (a form's shape is not the source's),
+ * ALIAS, UNSUPPORTED (2^31 tiles of 128 x 128 or more), CUDA. */
+MUON_API muon_status_t muon_fp4_quantize(const muon_fp4_source_t* src, void* stream);
+
+/* dst [rows, k] (row pitch ld elements, dst_dtype) = the values of a 4-bit
+ * matrix, asynchronously on `stream`; exact in fp32 and, as long as the
+ * exponent is in range, in bf16.  Errors: INVALID_ARG, ALIAS, UNSUPPORTED, CUDA. */
+MUON_API muon_status_t muon_fp4_dequantize(const muon_fp4_matrix_t* m, void* dst, int64_t ld, int32_t dst_dtype,
+                                           void* stream);
+
+/* A plan that quantises a fixed list of sources (one source dtype, one format,
+ * the same forms for all) in one pass, whatever their count: the 4-bit copies
+ * of a model's weights after an optimizer step.  The pointers are kept; the
+ * caller keeps the buffers alive.  values_dtype >= 0: muon_fp4_values also
+ * writes every form's values, to values_cols / values_rows.  Uploads its
+ * tables with synchronous copies.  Errors: as muon_fp4_quantize, NO_MEMORY.
+ * On error *out is NULL. */
+typedef struct muon_fp4_plan_s* muon_fp4_plan_t;
+MUON_API muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs, int32_t n,
+                                     int32_t values_dtype, void* stream);
+
+/* Quantise every source of the plan, asynchronously on `stream`.  Errors:
+ * INVALID_ARG (NULL plan, or another device is current), CUDA. */
+MUON_API muon_status_t muon_fp4_run(muon_fp4_plan_t plan, void* stream);
+
+/* The values of every 4-bit matrix of the plan, asynchronously on `stream`.
+ * Errors: INVALID_ARG (also a plan without values), CUDA. */
+MUON_API muon_status_t muon_fp4_values(muon_fp4_plan_t plan, void* stream);
+
+/* Waits for the plan's last stream and frees it; NULL is ignored. */
+MUON_API void muon_fp4_destroy(muon_fp4_plan_t plan);
+
+/* out [a.rows, b.rows] (row pitch ldo elements, out_dtype) = A B^T, or with
+ * accumulate = 1 (fp32 only) out + A B^T, of two 4-bit matrices of one format
+ * and one k, asynchronously on `stream`: 4-bit tensor-core products with fp32
+ * sums, times g_A g_B (NV).  k = 0 gives zeros (out as it is with accumulate).
+ * Rows of padding between ldo and b.rows are not written.  A NaN scale makes
+ * its row (A) or column (B) of out NaN.
+ * The call uses no workspace; calls on several streams are independent.
+ * A device-side wait that gives up is reported by muon_fp4_get_status.
+ * Errors: INVALID_ARG, SHAPE_MISMATCH (k or format differ), ALIAS,
+ * UNSUPPORTED (not an sm_100 device), CUDA. */
+MUON_API muon_status_t muon_fp4_product(const muon_fp4_matrix_t* a, const muon_fp4_matrix_t* b, void* out, int64_t ldo,
+                                        int32_t out_dtype, int32_t accumulate, void* stream);
+
+/* out [t, w.rows] (row pitch ldo elements, out_dtype) = X W^T for a few rows X
+ * [t, w.k] in bf16 (row pitch ldx elements), 0 <= t <= MUON_FP4_MAX_ROWS, and
+ * a 4-bit matrix W, asynchronously on `stream`: the form for single tokens,
+ * in which X keeps its precision and a row's result does not depend on the
+ * other rows.  fp32 sums.  Errors: INVALID_ARG, ALIAS, CUDA. */
+#define MUON_FP4_MAX_ROWS 32
+MUON_API muon_status_t muon_fp4_rows_product(const void* x, int64_t t, int64_t ldx, const muon_fp4_matrix_t* w,
+                                             void* out, int64_t ldo, int32_t out_dtype, void* stream);
+
+/* Synchronizes `stream`, then returns and clears the current device's sticky
+ * status of the muon_fp4_product calls: MUON_OK, or MUON_ERR_TIMEOUT after a
+ * device-side wait gave up (the outputs of that call are invalid).
+ * CUDA errors: MUON_ERR_CUDA. */
+MUON_API muon_status_t muon_fp4_get_status(void* stream);
+
 #ifdef __cplusplus
 }
 #endif

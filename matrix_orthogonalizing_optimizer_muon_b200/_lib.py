@@ -37,6 +37,8 @@ MUON_PROFILE_LAUNCHES = 1
 MUON_PROFILE_SPANS = 2
 PHASE_NAMES = ("momentum_normalise", "gram", "poly", "x_update", "finalize", "newton_schulz")
 ENTROPY_NUM_PHASES = 4
+MUON_FP4_NONE, MUON_FP4_MX, MUON_FP4_NV = -1, 0, 1
+MUON_FP4_MAX_ROWS = 32
 
 EXPORTED = ("muon_hparams_default", "muon_init", "muon_init_ex", "muon_num_waves", "muon_inject_wait_timeout",
             "muon_step", "muon_orthogonalize", "muon_workspace_bytes",
@@ -44,7 +46,9 @@ EXPORTED = ("muon_hparams_default", "muon_init", "muon_init_ex", "muon_num_waves
             "muon_orthogonalize_noalloc", "muon_adamw_hparams_default", "muon_adamw_init", "muon_adamw_step",
             "muon_adamw_destroy", "muon_entropy_init", "muon_entropy_compute", "muon_entropy_num_singular_values", "muon_entropy_cluster_size",
             "muon_entropy_get_status", "muon_entropy_profile", "muon_entropy_destroy", "muon_pack_init",
-            "muon_pack_run", "muon_pack_destroy")
+            "muon_pack_run", "muon_pack_destroy", "muon_fp4_sizes", "muon_fp4_quantize", "muon_fp4_dequantize",
+            "muon_fp4_init", "muon_fp4_run", "muon_fp4_values", "muon_fp4_destroy", "muon_fp4_product",
+            "muon_fp4_rows_product", "muon_fp4_get_status")
 
 
 class muon_param_t(ctypes.Structure):
@@ -73,6 +77,19 @@ class muon_adamw_param_t(ctypes.Structure):
 class muon_adamw_hparams_t(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("step", ctypes.c_int32)]
+
+
+class muon_fp4_matrix_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("tensor_scale", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("k", ctypes.c_int64), ("format", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class muon_fp4_source_t(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("ld", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("src_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("along_cols", muon_fp4_matrix_t), ("along_rows", muon_fp4_matrix_t),
+                ("values_cols", ctypes.c_void_p), ("values_rows", ctypes.c_void_p)]
 
 
 class MuonError(RuntimeError):
@@ -156,6 +173,29 @@ def load() -> ctypes.CDLL:
     lib.muon_entropy_profile.restype = ctypes.c_int
     lib.muon_entropy_destroy.argtypes = [P]
     lib.muon_entropy_destroy.restype = None
+    M = ctypes.POINTER(muon_fp4_matrix_t)
+    S = ctypes.POINTER(muon_fp4_source_t)
+    lib.muon_fp4_sizes.argtypes = [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64),
+                                   ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)]
+    lib.muon_fp4_sizes.restype = ctypes.c_int
+    lib.muon_fp4_quantize.argtypes = [S, P]
+    lib.muon_fp4_quantize.restype = ctypes.c_int
+    lib.muon_fp4_dequantize.argtypes = [M, P, ctypes.c_int64, ctypes.c_int32, P]
+    lib.muon_fp4_dequantize.restype = ctypes.c_int
+    lib.muon_fp4_init.argtypes = [ctypes.POINTER(P), S, ctypes.c_int32, ctypes.c_int32, P]
+    lib.muon_fp4_init.restype = ctypes.c_int
+    lib.muon_fp4_run.argtypes = [P, P]
+    lib.muon_fp4_run.restype = ctypes.c_int
+    lib.muon_fp4_values.argtypes = [P, P]
+    lib.muon_fp4_values.restype = ctypes.c_int
+    lib.muon_fp4_destroy.argtypes = [P]
+    lib.muon_fp4_destroy.restype = None
+    lib.muon_fp4_product.argtypes = [M, M, P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, P]
+    lib.muon_fp4_product.restype = ctypes.c_int
+    lib.muon_fp4_rows_product.argtypes = [P, ctypes.c_int64, ctypes.c_int64, M, P, ctypes.c_int64, ctypes.c_int32, P]
+    lib.muon_fp4_rows_product.restype = ctypes.c_int
+    lib.muon_fp4_get_status.argtypes = [P]
+    lib.muon_fp4_get_status.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -314,3 +354,54 @@ def muon_entropy_profile(plan, enable: bool, read: bool = False):
 
 def muon_entropy_destroy(plan) -> None:
     load().muon_entropy_destroy(plan)
+
+
+def muon_fp4_sizes(fmt: int, rows: int, k: int):
+    """(pitch, bytes of the codes, bytes of the scales) of a 4-bit matrix."""
+    pitch, data, scales = ctypes.c_int64(), ctypes.c_size_t(), ctypes.c_size_t()
+    check(load().muon_fp4_sizes(int(fmt), int(rows), int(k), ctypes.byref(pitch), ctypes.byref(data),
+                                ctypes.byref(scales)), "muon_fp4_sizes")
+    return pitch.value, data.value, scales.value
+
+
+def muon_fp4_quantize(src: muon_fp4_source_t, stream: int) -> None:
+    check(load().muon_fp4_quantize(ctypes.byref(src), stream), "muon_fp4_quantize")
+
+
+def muon_fp4_dequantize(m: muon_fp4_matrix_t, dst_ptr: int, ld: int, dtype: int, stream: int) -> None:
+    check(load().muon_fp4_dequantize(ctypes.byref(m), dst_ptr, ld, dtype, stream), "muon_fp4_dequantize")
+
+
+def muon_fp4_init(srcs, n: int, values_dtype: int, stream: int) -> ctypes.c_void_p:
+    plan = ctypes.c_void_p()
+    check(load().muon_fp4_init(ctypes.byref(plan), srcs, int(n), int(values_dtype), ctypes.c_void_p(stream)),
+          "muon_fp4_init")
+    return plan
+
+
+def muon_fp4_run(plan, stream: int) -> None:
+    check(load().muon_fp4_run(plan, ctypes.c_void_p(stream)), "muon_fp4_run")
+
+
+def muon_fp4_values(plan, stream: int) -> None:
+    check(load().muon_fp4_values(plan, ctypes.c_void_p(stream)), "muon_fp4_values")
+
+
+def muon_fp4_destroy(plan) -> None:
+    load().muon_fp4_destroy(plan)
+
+
+def muon_fp4_product(a: muon_fp4_matrix_t, b: muon_fp4_matrix_t, out_ptr: int, ldo: int, out_dtype: int,
+                     accumulate: int, stream: int) -> None:
+    check(load().muon_fp4_product(ctypes.byref(a), ctypes.byref(b), out_ptr, ldo, out_dtype, accumulate, stream),
+          "muon_fp4_product")
+
+
+def muon_fp4_rows_product(x_ptr: int, t: int, ldx: int, w: muon_fp4_matrix_t, out_ptr: int, ldo: int, out_dtype: int,
+                          stream: int) -> None:
+    check(load().muon_fp4_rows_product(x_ptr, t, ldx, ctypes.byref(w), out_ptr, ldo, out_dtype, stream),
+          "muon_fp4_rows_product")
+
+
+def muon_fp4_get_status(stream: int) -> int:
+    return int(load().muon_fp4_get_status(ctypes.c_void_p(stream)))

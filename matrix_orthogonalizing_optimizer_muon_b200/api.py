@@ -14,7 +14,8 @@ step for them.
     adam = AdamWPlan([g.numel() for g in gains], states=[(m, v) ...])
     adam.step(list(zip(gains, grads, ms, vs)), step=t, lr=4.2e-4, weight_decay=0.1)
 
-``HybridStep`` runs both plans as one optimizer step.
+``HybridStep`` runs both plans as one optimizer step, and can refresh the
+4-bit copies of the weights (module ``fp4``) after it.
 
 Sec. 3.4 compares optimisers by the SVD entropy of the weight matrices;
 ``EntropyPlan`` computes it on the GPU.
@@ -299,7 +300,9 @@ class HybridStep:
     parameter and AdamW for the rest (RMSNorm gains, embedding, LM head), one
     learning rate and one weight decay for both; the RMSNorm gains keep their
     weight decay (Appendix D, "Training stability").  Both plans enqueue on
-    the same stream, Muon first; nothing waits on the host.
+    the same stream, Muon first; nothing waits on the host.  With `fp4` (an
+    ``fp4.Fp4Plan`` over the updated weights) every step ends by quantising
+    them to the 4-bit copies that the next forward and backward passes read.
 
         opt = HybridStep([W.shape for W in mats], [p.numel() for p in vecs],
                          momenta=Ms, adam_states=[(m, v), ...])
@@ -308,7 +311,8 @@ class HybridStep:
     """
 
     def __init__(self, matrix_shapes, vector_numels, *, momenta=None, adam_states=None, vector_g_dtypes=None,
-                 vector_decay=None, max_workspace_bytes: int | None = None, stream=None):
+                 vector_decay=None, max_workspace_bytes: int | None = None, fp4=None, stream=None):
+        self.fp4 = fp4
         self.muon = MuonPlan(matrix_shapes, momenta=momenta, max_workspace_bytes=max_workspace_bytes, stream=stream)
         self.adamw = AdamWPlan(vector_numels, g_dtypes=vector_g_dtypes, states=adam_states, stream=stream)
         self.vector_decay = list(vector_decay) if vector_decay is not None else None
@@ -323,6 +327,8 @@ class HybridStep:
                        coeffs=coeffs, update_rms=update_rms, stream=stream)
         self.adamw.step(vectors, step=t, lr=lr, weight_decay=weight_decay, betas=betas, eps=eps,
                         decay=self.vector_decay, stream=stream)
+        if self.fp4 is not None:
+            self.fp4.run(stream=stream)
 
     def status(self) -> int:
         return self.muon.status()

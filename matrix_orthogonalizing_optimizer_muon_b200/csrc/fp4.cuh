@@ -1,0 +1,195 @@
+// The 4-bit matrix format shared by the quantisation, product and few-row
+// kernels (declared in muon.h, muon_fp4_matrix_t).
+//
+// A row holds k values in blocks along k: e2m1 codes (bit 3 the sign, bits
+// 2..1 the exponent, bit 0 the mantissa) times their block's scale.
+//   MUON_FP4_MX  blocks of 32, scale 2^(byte - 127) (e8m0, 255 = NaN)
+//   MUON_FP4_NV  blocks of 16, scale e4m3(byte) * g, g one power of two per matrix
+// Codes are packed two a byte, lower k in the low four bits, rows at a pitch of
+// 16 ceil(k / 32) bytes (a TMA stride).  Scale bytes lie in atoms of 512
+// bytes, one for 128 rows x 4 blocks, so that an atom is one row-block's
+// share of a K step in the order in which the tensor core's scale memory takes
+// it: lane r % 32, 32-bit column r % 128 / 32, byte b % 4.
+#pragma once
+
+#include "muon.h"
+#include "muon_internal.cuh"
+
+#include <cuda_fp16.h>
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+namespace muon {
+namespace fp4 {
+
+constexpr int kAtomBytes = 512;
+constexpr int kAtomRows = 128;
+constexpr int64_t kMaxDim = int64_t(1) << 30;  // rows and k of one matrix
+
+__host__ __device__ constexpr int block_of(int format) { return format == MUON_FP4_NV ? 16 : 32; }
+__host__ __device__ constexpr int atom_k_of(int format) { return 4 * block_of(format); }
+__host__ __device__ inline int64_t pitch_of(int64_t k) { return (k + 31) / 32 * 16; }
+__host__ __device__ inline int64_t atoms_of(int format, int64_t k) {
+  return (k + atom_k_of(format) - 1) / atom_k_of(format);
+}
+inline int64_t row_blocks_of(int64_t rows) { return (rows + kAtomRows - 1) / kAtomRows; }
+inline size_t data_bytes_of(int64_t rows, int64_t k) { return static_cast<size_t>(rows) * pitch_of(k); }
+inline size_t scale_bytes_of(int format, int64_t rows, int64_t k) {
+  return static_cast<size_t>(row_blocks_of(rows)) * atoms_of(format, k) * kAtomBytes;
+}
+
+// Host: the fields of a descriptor are usable (sizes, format, pointers and
+// their alignment; a matrix without elements needs no pointers).
+inline bool valid(const muon_fp4_matrix_t& m) {
+  if (m.format != MUON_FP4_MX && m.format != MUON_FP4_NV) return false;
+  if (m.rows < 0 || m.k < 0 || m.rows > kMaxDim || m.k > kMaxDim || m.reserved != 0) return false;
+  if (m.rows == 0 || m.k == 0) return true;
+  if (m.data == nullptr || m.scales == nullptr) return false;
+  if (m.format == MUON_FP4_NV && m.tensor_scale == nullptr) return false;
+  return reinterpret_cast<uintptr_t>(m.data) % 16 == 0 && reinterpret_cast<uintptr_t>(m.scales) % 16 == 0 &&
+         reinterpret_cast<uintptr_t>(m.tensor_scale) % 4 == 0;
+}
+
+// A few byte ranges without an allocation (single-matrix calls); the list
+// calls use std::vector.
+struct RangeList {
+  ByteRange v[12];
+  int n = 0;
+  void push_back(const ByteRange& r) { v[n++] = r; }
+};
+
+template <class List>
+inline void add_ranges(const muon_fp4_matrix_t& m, List& v) {
+  if (m.rows == 0 || m.k == 0) return;
+  const uintptr_t d = reinterpret_cast<uintptr_t>(m.data), s = reinterpret_cast<uintptr_t>(m.scales);
+  v.push_back(ByteRange{d, d + data_bytes_of(m.rows, m.k)});
+  v.push_back(ByteRange{s, s + scale_bytes_of(m.format, m.rows, m.k)});
+  if (m.format == MUON_FP4_NV) {
+    const uintptr_t t = reinterpret_cast<uintptr_t>(m.tensor_scale);
+    v.push_back(ByteRange{t, t + 2 * sizeof(float)});
+  }
+}
+
+// true if two of `writes` meet, or one of `reads` meets one of them
+inline bool conflict(const RangeList& reads, const RangeList& writes) {
+  auto meet = [](const ByteRange& x, const ByteRange& y) { return x.lo < y.hi && y.lo < x.hi; };
+  for (int i = 0; i < writes.n; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (meet(writes.v[i], writes.v[j])) return true;
+    for (int j = 0; j < reads.n; ++j)
+      if (meet(writes.v[i], reads.v[j])) return true;
+  }
+  return false;
+}
+
+// the same over lists (sorts writes)
+inline bool conflict(const std::vector<ByteRange>& reads, std::vector<ByteRange>& writes) {
+  if (any_overlap(writes)) return true;
+  for (const ByteRange& r : reads) {
+    auto it = std::upper_bound(writes.begin(), writes.end(), r.lo,
+                               [](uintptr_t v, const ByteRange& x) { return v < x.lo; });
+    if (it != writes.end() && it->lo < r.hi) return true;
+    if (it != writes.begin() && (it - 1)->hi > r.lo) return true;
+  }
+  return false;
+}
+
+// Byte of row r, block b within its atom.
+__host__ __device__ __forceinline__ int atom_byte(int r, int b) {
+  return (r & 31) * 16 + ((r & 127) >> 5) * 4 + (b & 3);
+}
+
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+  // 2^(byte - 127): byte 0 is the subnormal 2^-127, byte 255 NaN
+  return byte == 0u ? __uint_as_float(0x00400000u)
+                    : byte == 255u ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(byte << 23);
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t byte) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3);
+  return __half2float(__half(h));
+}
+
+// Two codes (low four bits first) as their values.
+__device__ __forceinline__ float2 e2m1_pair(uint32_t byte) {
+  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
+  return __half22float2(__half2(h));
+}
+
+// Eight values to eight codes, v[0] in the lowest four bits: nearest, ties to
+// the even code, saturating at 6.
+__device__ __forceinline__ uint32_t e2m1_pack8(const float* v) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return w;
+}
+
+// The matrix's power of two: the least g = 2^e, e >= -100, with amax <= 2688 g,
+// so that the largest block scale amax / (6 g) is at most 448, e4m3's largest.
+// 2688 = 1.3125 * 2^11, so e follows from the bits of amax (a finite fp32).
+// The floor keeps every scale, its reciprocal and the remainders of the
+// division below normal.
+__host__ __device__ __forceinline__ int tensor_exponent(uint32_t amax_bits) {
+  const int e = static_cast<int>(amax_bits >> 23) - 127 - 11 + ((amax_bits & 0x7FFFFFu) > 0x280000u ? 1 : 0);
+  return e < -100 ? -100 : e;
+}
+
+// Scale of one block from the bits of its largest magnitude (anything at or
+// above the bits of infinity says that the block holds a NaN or an infinity).
+struct BlockScale {
+  uint32_t byte;  // the scale byte
+  float d, r;     // NV: the scale and its reciprocal (0, 0 for a zero scale)
+                  // MX: r alone, the exact reciprocal; 0 for a non-finite block
+};
+
+template <bool kNv>
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float g) {
+  BlockScale b;
+  b.d = 0.0f;
+  if (kNv) {
+    // amax / (6 g) is rounded twice, to fp32 and then to e4m3, with the result
+    // of one rounding: a quotient by 6 g (significand 1.5) that is not itself
+    // a midpoint of e4m3 (5 significant bits) lies more than half an fp32
+    // step from every midpoint.
+    const float q = __fdiv_rn(__uint_as_float(amax_bits), 6.0f * g);
+    b.byte = __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+    b.d = e4m3_value(b.byte) * g;  // exact: four significant bits
+    b.r = b.d > 0.0f ? __frcp_rn(b.d) : 0.0f;
+    if (amax_bits >= 0x7F800000u) {
+      b.byte = 0x7Fu;
+      b.d = b.r = 0.0f;
+    }
+  } else {
+    const int e = static_cast<int>(amax_bits >> 23) - 2;
+    b.byte = e < 0 ? 0u : static_cast<uint32_t>(e);
+    b.r = __uint_as_float((254u - b.byte) << 23);
+    if (amax_bits >= 0x7F800000u) {
+      b.byte = 255u;
+      b.r = 0.0f;
+    }
+  }
+  return b;
+}
+
+// x divided by the block's scale, such that the rounding to e2m1 that follows
+// gives the code of the exact quotient.  MX: the product with a power of two
+// is exact.  NV: the quotient by d is corrected once by its remainder, which
+// gives d's multiples exactly and the rest to within an fp32 rounding; a
+// quotient by a four-bit d that is no midpoint of e2m1 (three significant
+// bits) is more than half an fp32 step from every midpoint.
+template <bool kNv>
+__device__ __forceinline__ float scaled(float x, const BlockScale& b) {
+  const float q = x * b.r;
+  if (!kNv) return q;
+  return fmaf(-fmaf(q, b.d, -x), b.r, q);  // in this form a zero keeps its sign
+}
+
+}  // namespace fp4
+}  // namespace muon

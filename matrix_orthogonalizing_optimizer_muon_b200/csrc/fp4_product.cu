@@ -1,0 +1,578 @@
+// Product of two 4-bit matrices, out[M, N] = A B^T (format: fp4.cuh), on the
+// 5th-generation tensor cores: sum over blocks of s_a s_b sum over the block
+// of the codes' products, block scaling done by the tensor core, fp32 sums.
+//
+// A tile of kCg * 128 x kBn outputs is computed by kCg CTAs (a 2-CTA pair
+// sharing one tcgen05.mma.cta_group::2, or one CTA).  Per CTA:
+//   warp 0      TMA producer: four lanes load a stage (256 of K: 128 bytes a
+//               row) of A's codes, B's codes, A's scales and B's scales; the
+//               scale atoms arrive in the order in which they are stored.
+//   warp 1      TMEM allocator; in the leading CTA one thread copies a
+//               stage's scale atoms to TMEM (tcgen05.cp, 32 lanes x 16 bytes,
+//               repeated for the four lane quadrants) and issues its four
+//               MMAs of K = 64.  A stage's scales have TMEM columns of their
+//               own, so they are overwritten only after the MMAs that read them
+//               have released the stage.
+//   warps 2..9  epilogue: the accumulator is drained to registers in one go
+//               (128 columns a thread), after which the next tile's MMAs may
+//               start while this tile is scaled, converted and stored.  Two
+//               accumulators and the scales do not fit into TMEM's 512 columns.
+#include "fp4.cuh"
+#include "tc_ptx.cuh"
+
+#include <cuda.h>
+
+namespace {
+
+using namespace muon;
+using namespace muon::fp4;
+
+__device__ unsigned g_fp4_status;  // kStatusTimeout, sticky until muon_fp4_get_status
+
+constexpr int kThreadsP = 320;
+constexpr int kEpi0 = 2;            // first epilogue warp
+constexpr int kEpiWarpsP = 8;
+constexpr int kStageK = 256;        // K of a stage: one 128-byte swizzle atom of codes
+constexpr int kRowBytes = 128;      // codes of a row in a stage
+constexpr int kMmaK = 64;           // K of one MMA
+
+__host__ __device__ constexpr int atoms_per_stage(bool nv) { return nv ? 4 : 2; }
+
+template <int kCg, int kBn, bool kNv>
+struct Cfg {
+  static constexpr int kAtoms = atoms_per_stage(kNv);
+  static constexpr int kABytes = 128 * kRowBytes;
+  static constexpr int kBRows = kBn / kCg;  // B rows staged by one CTA
+  static constexpr int kBBytes = kBRows * kRowBytes;
+  static constexpr int kSaBytes = kAtoms * kAtomBytes;
+  static constexpr int kSbBytes = kAtoms * kAtomBytes * (kBn / 128);  // every CTA needs the scales of all kBn columns
+  static constexpr int kStage = kABytes + kBBytes + kSaBytes + kSbBytes;
+  static constexpr int kStages = kBn == 256 ? 5 : 5;
+  static constexpr int kBar = kStages * kStage;
+  static constexpr int kMisc = kBar + (2 * kStages + 3) * 8;
+  static constexpr int kSmem = kMisc + 16 + 1024;
+  static constexpr uint32_t kTx = static_cast<uint32_t>(kCg) * kStage;
+  // TMEM columns: accumulator, then per stage the scales of A and of B
+  static constexpr int kSfStage = kAtoms * 4 * (1 + kBn / 128);
+  static constexpr int kSf0 = kBn;
+  static constexpr int kCols = 512;
+  static_assert(kSf0 + kStages * kSfStage <= kCols, "TMEM");
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kStage % 1024 == 0, "swizzle atoms");
+};
+
+struct ProdArgs {
+  void* out;
+  int64_t ldo;
+  const float* ga;
+  const float* gb;
+  int32_t m, n, nk, tiles_m, tiles_n;
+  int32_t out_dtype, accumulate, vec;
+};
+
+template <int kCg>
+__device__ __forceinline__ void tma_load(uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+  if (kCg == 2) {
+    tma_load_pair(dst, map, x, y, bar);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  }
+}
+
+// arrive on the barrier at this offset in every CTA of the tile once this
+// thread's earlier tensor-core work is done
+template <int kCg>
+__device__ __forceinline__ void commit_all(uint32_t bar) {
+  if (kCg == 2) tc_commit_pair(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Scale atom (512 bytes of shared memory: 32 rows of 16 bytes) to four TMEM columns.
+template <int kCg>
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+  if (kCg == 2) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+  else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+template <int kCg, bool kNv>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                        uint32_t acc) {
+#define MUON_FP4_MMA(cg, kind, vec)                                                                             \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::" cg ".kind::" kind       \
+               ".block_scale.scale_vec::" vec " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                \
+               "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)                                           \
+               : "memory")
+  if (kNv) {
+    if (kCg == 2) MUON_FP4_MMA("2", "mxf4nvf4", "4X");
+    else MUON_FP4_MMA("1", "mxf4nvf4", "4X");
+  } else {
+    if (kCg == 2) MUON_FP4_MMA("2", "mxf4", "2X");
+    else MUON_FP4_MMA("1", "mxf4", "2X");
+  }
+#undef MUON_FP4_MMA
+}
+
+// 128-byte-swizzled K-major operand: eight rows of 128 bytes every 1024
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// unswizzled scale atom: eight rows of 16 bytes every 128
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t(128 >> 4) << 32) |
+         (uint64_t(1) << 46);
+}
+
+// Instruction descriptor of the 4-bit kinds: e2m1 x e2m1 (1 at bits 7 and
+// 10), N / 8 at 17, scale type at 23 (1: e8m0, 0: e4m3), M / 16 at 24; the
+// byte of a scale column's word from which A's and B's scales are taken at 29
+// and 4.
+template <int kCg, int kBn, bool kNv>
+__device__ __forceinline__ uint32_t make_idesc_fp4(uint32_t sf_id) {
+  return (sf_id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kBn >> 3) << 17) | ((kNv ? 0u : 1u) << 23) |
+         (static_cast<uint32_t>((128 * kCg) >> 4) << 24) | (sf_id << 29);
+}
+
+// Tile t in an order that keeps eight rows of tiles together, so that the
+// tiles in flight share operands in L2.
+__device__ __forceinline__ void tile_place(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
+  constexpr int kGroup = 8;
+  const int per = kGroup * tiles_n;
+  const int g = t / per, first = g * kGroup;
+  const int rows = min(kGroup, tiles_m - first);
+  const int r = t - g * per;
+  tm = first + r % rows;
+  tn = r / rows;
+}
+
+__device__ __forceinline__ void give_up(volatile int* abort_flag) {
+  *abort_flag = 1;
+  atomicOr(&g_fp4_status, kStatusTimeout);
+}
+
+template <int kCg, int kBn, bool kNv>
+__global__ void __launch_bounds__(kThreadsP, 1)
+    fp4_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                       const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb,
+                       const ProdArgs g) {
+  using C = Cfg<kCg, kBn, kNv>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::kBar;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (C::kStages + s); };
+  const uint32_t tfull_bar = bar0 + 8u * (2 * C::kStages);
+  const uint32_t tempty_bar = tfull_bar + 8u;
+  const uint32_t drain_bar = tfull_bar + 16u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = kCg == 2 ? cta_rank() : 0u;
+  const bool leader = rank == 0u;
+  const int unit = static_cast<int>(blockIdx.x) / kCg, nunits = static_cast<int>(gridDim.x) / kCg;
+  const int ntiles = g.tiles_m * g.tiles_n;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(tfull_bar, 1);
+    mbar_init(tempty_bar, kCg * kEpiWarpsP);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    if (kCg == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                   "r"(C::kCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                   "r"(C::kCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (kCg == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const void* map = lane == 0 ? &map_a : lane == 1 ? &map_b : lane == 2 ? &map_sa : &map_sb;
+    if (lane < 4) prefetch_tensormap(map);
+    const uint32_t off = lane == 0 ? 0u
+                         : lane == 1 ? C::kABytes
+                         : lane == 2 ? C::kABytes + C::kBBytes
+                                     : C::kABytes + C::kBBytes + C::kSaBytes;
+    const int xstep = lane < 2 ? kRowBytes : C::kAtoms * (kAtomBytes / 8);
+    const uint32_t full0 = kCg == 2 ? map_to_rank(full_bar(0), 0) : full_bar(0);
+    int stage = 0;
+    uint32_t phase = 0;
+    long fills = 0;
+    for (int t = unit; t < ntiles; t += nunits) {
+      int tm, tn;
+      tile_place(t, g.tiles_m, g.tiles_n, tm, tn);
+      const int row_block = tm * kCg + static_cast<int>(rank);
+      const int y = lane == 0   ? row_block * 128
+                    : lane == 1 ? tn * kBn + static_cast<int>(rank) * C::kBRows
+                    : lane == 2 ? row_block
+                                : tn * (kBn / 128);
+      bool ok = true;
+      for (int kb = 0; kb < g.nk; ++kb, ++fills) {
+        int ready = 0;
+        if (lane == 0) {
+          ready = wait_hot(empty_bar(stage), phase ^ 1u, abort_flag) ? 1 : 0;
+          if (!ready) give_up(abort_flag);
+          else if (leader) mbar_arrive_expect_tx(full_bar(stage), C::kTx);
+        }
+        ready = __shfl_sync(0xffffffffu, ready, 0);
+        if (!ready) {
+          ok = false;
+          break;
+        }
+        if (lane < 4)
+          tma_load<kCg>(sbase + stage * C::kStage + off, map, kb * xstep, y, full0 + 8u * static_cast<uint32_t>(stage));
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+    }
+    // both CTAs' loads complete on the leader's barriers: the last fill of
+    // every stage has landed before any CTA leaves
+    if (leader && lane == 0) {
+      for (long f = fills > C::kStages ? fills - C::kStages : 0; f < fills; ++f)
+        if (!wait_bounded(full_bar(static_cast<int>(f % C::kStages)), static_cast<uint32_t>((f / C::kStages) & 1), nullptr))
+          atomicOr(&g_fp4_status, kStatusTimeout);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (leader && lane == 0) {
+      const uint64_t a0 = operand_desc(sbase), b0 = operand_desc(sbase + C::kABytes);
+      const uint64_t sa0 = scale_desc(sbase + C::kABytes + C::kBBytes);
+      const uint64_t sb0 = scale_desc(sbase + C::kABytes + C::kBBytes + C::kSaBytes);
+      int stage = 0;
+      uint32_t phase = 0, tphase = 0;
+      bool issued = false;
+      for (int t = unit; t < ntiles; t += nunits) {
+        if (!wait_bounded(tempty_bar, tphase ^ 1u, abort_flag)) {
+          give_up(abort_flag);
+          break;
+        }
+        tphase ^= 1u;
+        tc_fence_after();
+        bool ok = true;
+        for (int kb = 0; kb < g.nk; ++kb) {
+          if (!wait_hot(full_bar(stage), phase, abort_flag)) {
+            give_up(abort_flag);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t so = static_cast<uint64_t>((stage * C::kStage) >> 4);
+          const uint32_t sfa = tmem + C::kSf0 + stage * C::kSfStage;
+          const uint32_t sfb = sfa + C::kAtoms * 4;
+#pragma unroll
+          for (int k = 0; k < C::kAtoms; ++k) {
+            copy_scales<kCg>(sfa + 4 * k, sa0 + so + (k * kAtomBytes >> 4));
+#pragma unroll
+            for (int r = 0; r < kBn / 128; ++r)  // the two row blocks of B side by side
+              copy_scales<kCg>(sfb + k * 4 * (kBn / 128) + 4 * r,
+                               sb0 + so + ((r * C::kAtoms + k) * kAtomBytes >> 4));
+          }
+#pragma unroll
+          for (int kk = 0; kk < kStageK / kMmaK; ++kk) {
+            const int atom = kNv ? kk : kk >> 1;
+            mma_fp4<kCg, kNv>(tmem, a0 + so + (kk * 32 >> 4), b0 + so + (kk * 32 >> 4),
+                              make_idesc_fp4<kCg, kBn, kNv>(kNv ? 0u : (kk & 1) * 2u), sfa + 4 * atom,
+                              sfb + atom * 4 * (kBn / 128), (kb | kk) != 0 ? 1u : 0u);
+          }
+          issued = true;
+          commit_all<kCg>(empty_bar(stage));
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        commit_all<kCg>(tfull_bar);
+      }
+      if (issued) {
+        if (kCg == 2) tc_commit(drain_bar);
+        else commit_all<1>(drain_bar);
+        if (!wait_bounded(drain_bar, 0u, nullptr)) atomicOr(&g_fp4_status, kStatusTimeout);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3, half = (warp - kEpi0) >> 2;
+    constexpr int kPer = kBn / 2 / 32;  // 32-column chunks of a warp
+    const uint32_t tempty = kCg == 2 ? map_to_rank(tempty_bar, 0) : tempty_bar;
+    const float ga = kNv ? *g.ga : 1.0f, gb = kNv ? *g.gb : 1.0f;
+    uint32_t tphase = 0;
+    for (int t = unit; t < ntiles; t += nunits) {
+      const bool ready = wait_bounded(tfull_bar, tphase, abort_flag);
+      if (!__all_sync(0xffffffffu, ready)) {  // the warp leaves as one: tcgen05.ld is aligned
+        if (lane == 0) give_up(abort_flag);
+        break;
+      }
+      tphase ^= 1u;
+      tc_fence_after();
+      uint32_t v[kPer][32];
+#pragma unroll
+      for (int c = 0; c < kPer; ++c)
+        tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * (kBn / 2) + c * 32, v[c]);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty);
+      int tm, tn;
+      tile_place(t, g.tiles_m, g.tiles_n, tm, tn);
+      const int row = (tm * kCg + static_cast<int>(rank)) * 128 + quad * 32 + lane;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) {
+        const int col = tn * kBn + half * (kBn / 2) + c * 32;
+        if (row >= g.m || col >= g.n) continue;
+        float f[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = kNv ? __uint_as_float(v[c][i]) * ga * gb : __uint_as_float(v[c][i]);
+        if (g.out_dtype == MUON_DT_BF16) {
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(g.out) + static_cast<int64_t>(row) * g.ldo + col;
+          if (g.vec && col + 32 <= g.n) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              __align__(16) __nv_bfloat162 h[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[8 * q + 2 * i], f[8 * q + 2 * i + 1]);
+              reinterpret_cast<uint4*>(o)[q] = *reinterpret_cast<const uint4*>(h);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (col + i < g.n) o[i] = __float2bfloat16_rn(f[i]);
+          }
+        } else {
+          float* o = static_cast<float*>(g.out) + static_cast<int64_t>(row) * g.ldo + col;
+          if (g.vec && col + 32 <= g.n) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              float4 w = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+              if (g.accumulate) {
+                const float4 p = reinterpret_cast<const float4*>(o)[q];
+                w.x += p.x;
+                w.y += p.y;
+                w.z += p.z;
+                w.w += p.w;
+              }
+              reinterpret_cast<float4*>(o)[q] = w;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (col + i < g.n) o[i] = g.accumulate ? o[i] + f[i] : f[i];
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (kCg == 2) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    if (kCg == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- host
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = []() -> EncodeFn {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// Codes of a 4-bit matrix: boxes of 128 bytes x `rows` rows, 128-byte swizzle,
+// zeros past the edges.
+bool encode_codes(CUtensorMap* tm, const muon_fp4_matrix_t& m, int rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(pitch_of(m.k)), static_cast<cuuint64_t>(m.rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch_of(m.k))};
+  const cuuint32_t box[2] = {kRowBytes, static_cast<cuuint32_t>(rows)};
+  const cuuint32_t es[2] = {1, 1};
+  return encode_fn()(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, m.data, dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Scale atoms as rows of 8-byte words: boxes of a stage's atoms x `blocks`
+// row blocks, zeros (a scale of 0, or 2^-127 on codes that are 0) past the edges.
+bool encode_scales(CUtensorMap* tm, const muon_fp4_matrix_t& m, int blocks) {
+  const int64_t atoms = atoms_of(m.format, m.k);
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(atoms) * (kAtomBytes / 8),
+                              static_cast<cuuint64_t>(row_blocks_of(m.rows))};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(atoms) * kAtomBytes};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(atoms_per_stage(m.format == MUON_FP4_NV) * (kAtomBytes / 8)),
+                             static_cast<cuuint32_t>(blocks)};
+  const cuuint32_t es[2] = {1, 1};
+  return encode_fn()(tm, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, m.scales, dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct DeviceInfo {
+  bool ok;
+  int sms;
+};
+
+// Read once per device; the calls that follow touch no device state.
+const DeviceInfo& device_info(int dev) {
+  static const struct All {
+    DeviceInfo d[64];
+    All() {
+      int n = 0;
+      if (cudaGetDeviceCount(&n) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+      }
+      for (int i = 0; i < 64; ++i) {
+        d[i] = {false, 0};
+        int major = 0;
+        if (i < n && cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, i) == cudaSuccess && major == 10 &&
+            cudaDeviceGetAttribute(&d[i].sms, cudaDevAttrMultiProcessorCount, i) == cudaSuccess)
+          d[i].ok = true;
+      }
+    }
+  } all;
+  static const DeviceInfo none{false, 0};
+  return dev >= 0 && dev < 64 ? all.d[dev] : none;
+}
+
+template <int kCg, int kBn, bool kNv>
+muon_status_t launch_product(const muon_fp4_matrix_t& a, const muon_fp4_matrix_t& b, ProdArgs g, int sms,
+                             cudaStream_t st) {
+  using C = Cfg<kCg, kBn, kNv>;
+  CUtensorMap ma, mb, msa, msb;
+  if (!encode_codes(&ma, a, 128) || !encode_codes(&mb, b, C::kBRows) || !encode_scales(&msa, a, 1) ||
+      !encode_scales(&msb, b, kBn / 128))
+    return MUON_ERR_CUDA;
+  auto kernel = fp4_product_kernel<kCg, kBn, kNv>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+    return MUON_ERR_CUDA;
+  g.tiles_m = (g.m + kCg * 128 - 1) / (kCg * 128);
+  g.tiles_n = (g.n + kBn - 1) / kBn;
+  const int64_t tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
+  if (tiles > 0x3fffffff) return MUON_ERR_UNSUPPORTED;
+  const int64_t units = tiles < sms / kCg ? tiles : sms / kCg;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * kCg));
+  cfg.blockDim = dim3(kThreadsP);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCg;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, ma, mb, msa, msb, g) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status_t muon_fp4_product(const muon_fp4_matrix_t* a, const muon_fp4_matrix_t* b, void* out, int64_t ldo,
+                               int32_t out_dtype, int32_t accumulate, void* stream) {
+  if (a == nullptr || b == nullptr || !valid(*a) || !valid(*b)) return MUON_ERR_INVALID_ARG;
+  if (out_dtype != MUON_DT_BF16 && out_dtype != MUON_DT_FP32) return MUON_ERR_INVALID_ARG;
+  if ((accumulate != 0 && accumulate != 1) || (accumulate && out_dtype != MUON_DT_FP32)) return MUON_ERR_INVALID_ARG;
+  if (a->k != b->k || a->format != b->format) return MUON_ERR_SHAPE_MISMATCH;
+  if (a->rows == 0 || b->rows == 0) return MUON_OK;
+  const int es = out_dtype == MUON_DT_BF16 ? 2 : 4;
+  const uintptr_t o = reinterpret_cast<uintptr_t>(out);
+  if (out == nullptr || o % es != 0 || ldo < b->rows || ldo > (int64_t(1) << 40)) return MUON_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a->k == 0) {
+    if (accumulate) return MUON_OK;
+    return cudaMemset2DAsync(out, static_cast<size_t>(ldo) * es, 0, static_cast<size_t>(b->rows) * es,
+                             static_cast<size_t>(a->rows), st) == cudaSuccess
+               ? MUON_OK
+               : MUON_ERR_CUDA;
+  }
+  RangeList reads, writes;
+  add_ranges(*a, reads);
+  add_ranges(*b, reads);
+  writes.push_back(ByteRange{o, o + (static_cast<size_t>(a->rows - 1) * ldo + b->rows) * es});
+  if (conflict(reads, writes)) return MUON_ERR_ALIAS;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MUON_ERR_CUDA;
+  const DeviceInfo& info = device_info(dev);
+  if (!info.ok) return MUON_ERR_UNSUPPORTED;
+  if (encode_fn() == nullptr) return MUON_ERR_CUDA;
+  ProdArgs g = {};
+  g.out = out;
+  g.ldo = ldo;
+  g.ga = a->tensor_scale;
+  g.gb = b->tensor_scale;
+  g.m = static_cast<int32_t>(a->rows);
+  g.n = static_cast<int32_t>(b->rows);
+  g.nk = static_cast<int32_t>((a->k + kStageK - 1) / kStageK);
+  g.out_dtype = out_dtype;
+  g.accumulate = accumulate;
+  g.vec = (o % 16 == 0 && ldo * es % 16 == 0) ? 1 : 0;
+  const bool nv = a->format == MUON_FP4_NV;
+  // pairs where there are enough 256 x 256 tiles for them, single CTAs below
+  const int64_t pair_tiles = ((a->rows + 255) / 256) * ((b->rows + 255) / 256);
+  if (pair_tiles >= info.sms / 4)
+    return nv ? launch_product<2, 256, true>(*a, *b, g, info.sms, st)
+              : launch_product<2, 256, false>(*a, *b, g, info.sms, st);
+  return nv ? launch_product<1, 128, true>(*a, *b, g, info.sms, st)
+            : launch_product<1, 128, false>(*a, *b, g, info.sms, st);
+}
+
+muon_status_t muon_fp4_get_status(void* stream) {
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return MUON_ERR_CUDA;
+  }
+  unsigned v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_fp4_status, sizeof(v)) != cudaSuccess ||
+      (v != 0 && cudaMemcpyToSymbol(g_fp4_status, &zero, sizeof(zero)) != cudaSuccess)) {
+    cudaGetLastError();
+    return MUON_ERR_CUDA;
+  }
+  return (v & kStatusTimeout) ? MUON_ERR_TIMEOUT : MUON_OK;
+}
+
+}  // extern "C"
