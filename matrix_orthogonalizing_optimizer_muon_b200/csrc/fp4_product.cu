@@ -4,19 +4,26 @@
 //
 // A tile of kCg * 128 x kBn outputs is computed by kCg CTAs (a 2-CTA pair
 // sharing one tcgen05.mma.cta_group::2, or one CTA).  Per CTA:
-//   warp 0      TMA producer: four lanes load a stage (256 of K: 128 bytes a
-//               row) of A's codes, B's codes, A's scales and B's scales; the
-//               scale atoms arrive in the order in which they are stored.
-//   warp 1      TMEM allocator; in the leading CTA one thread copies a
-//               stage's scale atoms to TMEM (tcgen05.cp, 32 lanes x 16 bytes,
-//               repeated for the four lane quadrants) and issues its four
-//               MMAs of K = 64.  A stage's scales have TMEM columns of their
-//               own, so they are overwritten only after the MMAs that read them
-//               have released the stage.
-//   warps 2..9  epilogue: the accumulator is drained to registers in one go
-//               (128 columns a thread), after which the next tile's MMAs may
-//               start while this tile is scaled, converted and stored.  Two
-//               accumulators and the scales do not fit into TMEM's 512 columns.
+//   warp 0       TMA producer: four lanes load a stage (256 of K: 128 bytes a
+//                row) of A's codes, B's codes, A's scales and B's scales; the
+//                scale atoms arrive in the order in which they are stored.
+//   warp 1       TMEM allocator; in the leading CTA the warp copies a stage's
+//                scale atoms to TMEM (tcgen05.cp, 32 lanes x 16 bytes, repeated
+//                for the four lane quadrants) and issues its four MMAs of
+//                K = 64, all from one elected lane: 17 tcgen05 instructions a
+//                stage.  Issued under `lane == 0` instead, each took about 75
+//                cycles and 8192^3 332 us; elected, 211 us.  A stage's scales
+//                have TMEM columns of their own, so they are overwritten only
+//                after the MMAs that read them have released the stage.
+//   warps 2..9   epilogue: a warp takes 32 rows and half the columns, 32 x 32
+//                blocks at a time, scales and converts them and stores each
+//                from a staging block by TMA (added in fp32 by the TMA's
+//                reduction), or, where the output's rows do not start or end
+//                on 16-byte boundaries (TMA writes whole 16-byte pieces), by
+//                rows of the block.  Two
+//                accumulators and the scales do not fit into TMEM's 512
+//                columns, so bf16 outputs are packed in registers and the
+//                accumulator is released before any of them is stored.
 #include "fp4.cuh"
 #include "tc_ptx.cuh"
 
@@ -32,6 +39,7 @@ __device__ unsigned g_fp4_status;  // kStatusTimeout, sticky until muon_fp4_get_
 constexpr int kThreadsP = 320;
 constexpr int kEpi0 = 2;            // first epilogue warp
 constexpr int kEpiWarpsP = 8;
+constexpr int kStagingBytes = 32 * 32 * 4;  // an epilogue warp's block of 32 x 32 outputs
 constexpr int kStageK = 256;        // K of a stage: one 128-byte swizzle atom of codes
 constexpr int kRowBytes = 128;      // codes of a row in a stage
 constexpr int kMmaK = 64;           // K of one MMA
@@ -48,7 +56,8 @@ struct Cfg {
   static constexpr int kSbBytes = kAtoms * kAtomBytes * (kBn / 128);  // every CTA needs the scales of all kBn columns
   static constexpr int kStage = kABytes + kBBytes + kSaBytes + kSbBytes;
   static constexpr int kStages = kBn == 256 ? 5 : 5;
-  static constexpr int kBar = kStages * kStage;
+  static constexpr int kEpi = kStages * kStage;
+  static constexpr int kBar = kEpi + kEpiWarpsP * kStagingBytes;
   static constexpr int kMisc = kBar + (2 * kStages + 3) * 8;
   static constexpr int kSmem = kMisc + 16 + 1024;
   static constexpr uint32_t kTx = static_cast<uint32_t>(kCg) * kStage;
@@ -83,6 +92,14 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const void* map, int x, i
   }
 }
 
+// true in one lane of a converged warp; the code under it keeps its operands
+// in uniform registers, which tcgen05 instructions take
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0u;
+}
+
 // arrive on the barrier at this offset in every CTA of the tile once this
 // thread's earlier tensor-core work is done
 template <int kCg>
@@ -90,6 +107,19 @@ __device__ __forceinline__ void commit_all(uint32_t bar) {
   if (kCg == 2) tc_commit_pair(bar);
   else
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// wait until all but this thread's last kN bulk stores have read shared memory
+template <int kN>
+__device__ __forceinline__ void bulk_wait_read_but() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kN) : "memory");
+}
+
+// TMA reduction of a staged box: global += shared, in fp32
+__device__ __forceinline__ void tma_add_2d(const void* map, uint32_t src, int x, int y) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
 }
 
 // Scale atom (512 bytes of shared memory: 32 rows of 16 bytes) to four TMEM columns.
@@ -159,7 +189,7 @@ template <int kCg, int kBn, bool kNv>
 __global__ void __launch_bounds__(kThreadsP, 1)
     fp4_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                        const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb,
-                       const ProdArgs g) {
+                       const __grid_constant__ CUtensorMap map_o, const ProdArgs g) {
   using C = Cfg<kCg, kBn, kNv>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -263,68 +293,71 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (leader && lane == 0) {
+    if (leader) {
       const uint64_t a0 = operand_desc(sbase), b0 = operand_desc(sbase + C::kABytes);
       const uint64_t sa0 = scale_desc(sbase + C::kABytes + C::kBBytes);
       const uint64_t sb0 = scale_desc(sbase + C::kABytes + C::kBBytes + C::kSaBytes);
       int stage = 0;
       uint32_t phase = 0, tphase = 0;
-      bool issued = false;
-      for (int t = unit; t < ntiles; t += nunits) {
-        if (!wait_bounded(tempty_bar, tphase ^ 1u, abort_flag)) {
-          give_up(abort_flag);
-          break;
-        }
+      bool issued = false, ok = true;
+      for (int t = unit; t < ntiles && ok; t += nunits) {
+        ok = __all_sync(0xffffffffu, wait_bounded(tempty_bar, tphase ^ 1u, abort_flag));
+        if (!ok) break;
         tphase ^= 1u;
         tc_fence_after();
-        bool ok = true;
         for (int kb = 0; kb < g.nk; ++kb) {
-          if (!wait_hot(full_bar(stage), phase, abort_flag)) {
-            give_up(abort_flag);
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, wait_hot(full_bar(stage), phase, abort_flag));
+          if (!ok) break;
           tc_fence_after();
-          const uint64_t so = static_cast<uint64_t>((stage * C::kStage) >> 4);
-          const uint32_t sfa = tmem + C::kSf0 + stage * C::kSfStage;
-          const uint32_t sfb = sfa + C::kAtoms * 4;
+          if (elect_one()) {
+            const uint64_t so = static_cast<uint64_t>((stage * C::kStage) >> 4);
+            const uint32_t sfa = tmem + C::kSf0 + stage * C::kSfStage;
+            const uint32_t sfb = sfa + C::kAtoms * 4;
 #pragma unroll
-          for (int k = 0; k < C::kAtoms; ++k) {
-            copy_scales<kCg>(sfa + 4 * k, sa0 + so + (k * kAtomBytes >> 4));
+            for (int k = 0; k < C::kAtoms; ++k) {
+              copy_scales<kCg>(sfa + 4 * k, sa0 + so + (k * kAtomBytes >> 4));
 #pragma unroll
-            for (int r = 0; r < kBn / 128; ++r)  // the two row blocks of B side by side
-              copy_scales<kCg>(sfb + k * 4 * (kBn / 128) + 4 * r,
-                               sb0 + so + ((r * C::kAtoms + k) * kAtomBytes >> 4));
+              for (int r = 0; r < kBn / 128; ++r)  // the two row blocks of B side by side
+                copy_scales<kCg>(sfb + k * 4 * (kBn / 128) + 4 * r,
+                                 sb0 + so + ((r * C::kAtoms + k) * kAtomBytes >> 4));
+            }
+#pragma unroll
+            for (int kk = 0; kk < kStageK / kMmaK; ++kk) {
+              const int atom = kNv ? kk : kk >> 1;
+              mma_fp4<kCg, kNv>(tmem, a0 + so + (kk * 32 >> 4), b0 + so + (kk * 32 >> 4),
+                                make_idesc_fp4<kCg, kBn, kNv>(kNv ? 0u : (kk & 1) * 2u), sfa + 4 * atom,
+                                sfb + atom * 4 * (kBn / 128), (kb | kk) != 0 ? 1u : 0u);
+            }
+            commit_all<kCg>(empty_bar(stage));
           }
-#pragma unroll
-          for (int kk = 0; kk < kStageK / kMmaK; ++kk) {
-            const int atom = kNv ? kk : kk >> 1;
-            mma_fp4<kCg, kNv>(tmem, a0 + so + (kk * 32 >> 4), b0 + so + (kk * 32 >> 4),
-                              make_idesc_fp4<kCg, kBn, kNv>(kNv ? 0u : (kk & 1) * 2u), sfa + 4 * atom,
-                              sfb + atom * 4 * (kBn / 128), (kb | kk) != 0 ? 1u : 0u);
-          }
+          __syncwarp();
           issued = true;
-          commit_all<kCg>(empty_bar(stage));
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (!ok) break;
-        commit_all<kCg>(tfull_bar);
+        if (ok && elect_one()) commit_all<kCg>(tfull_bar);
+        __syncwarp();
       }
+      if (!ok && lane == 0) give_up(abort_flag);
       if (issued) {
-        if (kCg == 2) tc_commit(drain_bar);
-        else commit_all<1>(drain_bar);
+        if (elect_one()) {
+          if (kCg == 2) tc_commit(drain_bar);
+          else commit_all<1>(drain_bar);
+        }
+        __syncwarp();
         if (!wait_bounded(drain_bar, 0u, nullptr)) atomicOr(&g_fp4_status, kStatusTimeout);
       }
     }
   } else {
     // ------------------------------------------------------------ epilogue
     const int quad = warp & 3, half = (warp - kEpi0) >> 2;
-    constexpr int kPer = kBn / 2 / 32;  // 32-column chunks of a warp
+    constexpr int kPer = kBn / 2 / 32;  // 32-column blocks of a warp
     const uint32_t tempty = kCg == 2 ? map_to_rank(tempty_bar, 0) : tempty_bar;
     const float ga = kNv ? *g.ga : 1.0f, gb = kNv ? *g.gb : 1.0f;
+    const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * (kBn / 2);
+    uint8_t* stg = smem + C::kEpi + (warp - kEpi0) * kStagingBytes;
     uint32_t tphase = 0;
     for (int t = unit; t < ntiles; t += nunits) {
       const bool ready = wait_bounded(tfull_bar, tphase, abort_flag);
@@ -334,63 +367,118 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       }
       tphase ^= 1u;
       tc_fence_after();
-      uint32_t v[kPer][32];
-#pragma unroll
-      for (int c = 0; c < kPer; ++c)
-        tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * (kBn / 2) + c * 32, v[c]);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty);
       int tm, tn;
       tile_place(t, g.tiles_m, g.tiles_n, tm, tn);
-      const int row = (tm * kCg + static_cast<int>(rank)) * 128 + quad * 32 + lane;
+      const int row0 = (tm * kCg + static_cast<int>(rank)) * 128 + quad * 32;
+      const int col0 = tn * kBn + half * (kBn / 2);
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty);
+      };
+      if (g.out_dtype == MUON_DT_BF16) {
+        uint32_t h[kPer][16];
 #pragma unroll
-      for (int c = 0; c < kPer; ++c) {
-        const int col = tn * kBn + half * (kBn / 2) + c * 32;
-        if (row >= g.m || col >= g.n) continue;
-        float f[32];
+        for (int c = 0; c < kPer; ++c) {
+          uint32_t v[32];
+          tmem_ld32(tq + c * 32, v);
+          tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) f[i] = kNv ? __uint_as_float(v[c][i]) * ga * gb : __uint_as_float(v[c][i]);
-        if (g.out_dtype == MUON_DT_BF16) {
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(g.out) + static_cast<int64_t>(row) * g.ldo + col;
-          if (g.vec && col + 32 <= g.n) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              __align__(16) __nv_bfloat162 h[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[8 * q + 2 * i], f[8 * q + 2 * i + 1]);
-              reinterpret_cast<uint4*>(o)[q] = *reinterpret_cast<const uint4*>(h);
+          for (int i = 0; i < 16; ++i) {
+            float x = __uint_as_float(v[2 * i]), y = __uint_as_float(v[2 * i + 1]);
+            if (kNv) {
+              x = x * ga * gb;
+              y = y * ga * gb;
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (col + i < g.n) o[i] = __float2bfloat16_rn(f[i]);
+            const __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
+            h[c][i] = *reinterpret_cast<const uint32_t*>(&p);
           }
-        } else {
-          float* o = static_cast<float*>(g.out) + static_cast<int64_t>(row) * g.ldo + col;
-          if (g.vec && col + 32 <= g.n) {
+        }
+        release();
+        if (row0 >= g.m) continue;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              float4 w = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
-              if (g.accumulate) {
-                const float4 p = reinterpret_cast<const float4*>(o)[q];
-                w.x += p.x;
-                w.y += p.y;
-                w.z += p.z;
-                w.w += p.w;
-              }
-              reinterpret_cast<float4*>(o)[q] = w;
+        for (int c = 0; c < kPer; ++c) {
+          const int col = col0 + c * 32;
+          if (col >= g.n) continue;
+          if (g.vec && (col + 32 <= g.n || g.n % 8 == 0)) {
+            uint8_t* blk = stg + (c & 1) * (kStagingBytes / 2);
+            if (lane == 0) bulk_wait_read_but<1>();  // the store before the last has read its half
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(blk + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(h[c][4 * q], h[c][4 * q + 1], h[c][4 * q + 2], h[c][4 * q + 3]);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&map_o, smem_u32(blk), col, row0);
+              bulk_commit();
             }
           } else {
+            // rows of 17 words: a thread writes its row and reads a column without conflicts
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(g.out) + static_cast<int64_t>(row0) * g.ldo + col;
+            uint32_t* w = reinterpret_cast<uint32_t*>(stg);
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (col + i < g.n) o[i] = g.accumulate ? o[i] + f[i] : f[i];
+            for (int i = 0; i < 16; ++i) w[lane * 17 + i] = h[c][i];
+            __syncwarp();
+            const int nr = min(32, g.m - row0);
+            if (col + lane < g.n)
+              for (int r = 0; r < nr; ++r)
+                out[r * g.ldo + lane] = reinterpret_cast<const __nv_bfloat16*>(w + r * 17)[lane];
+            __syncwarp();
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < kPer; ++c) {
+          uint32_t v[32];
+          tmem_ld32(tq + c * 32, v);
+          tmem_ld_wait();
+          if (c == kPer - 1) release();
+          const int col = col0 + c * 32;
+          if (row0 >= g.m || col >= g.n) continue;
+          if (kNv) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * ga * gb);
+          }
+          if (lane == 0) bulk_wait_read();
+          __syncwarp();
+          if (g.vec && (col + 32 <= g.n || g.n % 4 == 0)) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<uint4*>(stg + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                  make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              if (g.accumulate) tma_add_2d(&map_o, smem_u32(stg), col, row0);
+              else tma_store_2d(&map_o, smem_u32(stg), col, row0);
+              bulk_commit();
+            }
+          } else {
+            float* out = static_cast<float*>(g.out) + static_cast<int64_t>(row0) * g.ldo + col;
+            uint32_t* w = reinterpret_cast<uint32_t*>(stg);
+            // word i of row r at column i ^ r: conflict-free both ways
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[lane * 32 + (i ^ lane)] = v[i];
+            __syncwarp();
+            const int nr = min(32, g.m - row0);
+            if (col + lane < g.n) {
+#pragma unroll 8
+              for (int r = 0; r < nr; ++r) {
+                const float f = __uint_as_float(w[r * 32 + (lane ^ r)]);
+                out[r * g.ldo + lane] = g.accumulate ? out[r * g.ldo + lane] + f : f;
+              }
+            }
+            __syncwarp();
           }
         }
       }
-      __syncwarp();
     }
+    if (lane == 0) bulk_wait_all();  // the staging blocks are read, and the stores done, before the CTA leaves
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -449,6 +537,19 @@ bool encode_scales(CUtensorMap* tm, const muon_fp4_matrix_t& m, int blocks) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The output in blocks of 32 x 32, staged rows swizzled over the row's 64 or 128 bytes.
+bool encode_out(CUtensorMap* tm, const ProdArgs& g) {
+  const bool bf = g.out_dtype == MUON_DT_BF16;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.n), static_cast<cuuint64_t>(g.m)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(g.ldo) * (bf ? 2 : 4)};
+  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t es[2] = {1, 1};
+  return encode_fn()(tm, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, g.out, dims,
+                     strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     bf ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct DeviceInfo {
   bool ok;
   int sms;
@@ -481,9 +582,9 @@ template <int kCg, int kBn, bool kNv>
 muon_status_t launch_product(const muon_fp4_matrix_t& a, const muon_fp4_matrix_t& b, ProdArgs g, int sms,
                              cudaStream_t st) {
   using C = Cfg<kCg, kBn, kNv>;
-  CUtensorMap ma, mb, msa, msb;
+  CUtensorMap ma, mb, msa, msb, mo = {};
   if (!encode_codes(&ma, a, 128) || !encode_codes(&mb, b, C::kBRows) || !encode_scales(&msa, a, 1) ||
-      !encode_scales(&msb, b, kBn / 128))
+      !encode_scales(&msb, b, kBn / 128) || (g.vec && !encode_out(&mo, g)))
     return MUON_ERR_CUDA;
   auto kernel = fp4_product_kernel<kCg, kBn, kNv>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
@@ -505,7 +606,7 @@ muon_status_t launch_product(const muon_fp4_matrix_t& a, const muon_fp4_matrix_t
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, ma, mb, msa, msb, g) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, ma, mb, msa, msb, mo, g) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
 }  // namespace
@@ -550,7 +651,10 @@ muon_status_t muon_fp4_product(const muon_fp4_matrix_t* a, const muon_fp4_matrix
   g.nk = static_cast<int32_t>((a->k + kStageK - 1) / kStageK);
   g.out_dtype = out_dtype;
   g.accumulate = accumulate;
-  g.vec = (o % 16 == 0 && ldo * es % 16 == 0) ? 1 : 0;
+  // TMA stores take rows on 16-byte boundaries at most 2^40 bytes apart (one row has no pitch to speak of)
+  const int64_t pitch = a->rows == 1 ? (b->rows + 7) / 8 * 8 : ldo;
+  g.vec = (o % 16 == 0 && pitch * es % 16 == 0 && pitch * es < (int64_t(1) << 40)) ? 1 : 0;
+  if (g.vec) g.ldo = pitch;
   const bool nv = a->format == MUON_FP4_NV;
   // pairs where there are enough 256 x 256 tiles for them, single CTAs below
   const int64_t pair_tiles = ((a->rows + 255) / 256) * ((b->rows + 255) / 256);
