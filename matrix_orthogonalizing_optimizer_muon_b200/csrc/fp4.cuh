@@ -94,6 +94,29 @@ inline bool conflict(const std::vector<ByteRange>& reads, std::vector<ByteRange>
   return false;
 }
 
+// Host: SMs of an sm_100 device, 0 for another; read once for all devices, so
+// the calls that follow touch no device state.
+inline int device_sms(int dev) {
+  static const struct All {
+    int sms[64];
+    All() {
+      int n = 0;
+      if (cudaGetDeviceCount(&n) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+      }
+      for (int i = 0; i < 64; ++i) {
+        sms[i] = 0;
+        int major = 0, count = 0;
+        if (i < n && cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, i) == cudaSuccess && major == 10 &&
+            cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, i) == cudaSuccess)
+          sms[i] = count;
+      }
+    }
+  } all;
+  return dev >= 0 && dev < 64 ? all.sms[dev] : 0;
+}
+
 // Byte of row r, block b within its atom.
 __host__ __device__ __forceinline__ int atom_byte(int r, int b) {
   return (r & 31) * 16 + ((r & 127) >> 5) * 4 + (b & 3);

@@ -550,34 +550,6 @@ bool encode_out(CUtensorMap* tm, const ProdArgs& g) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct DeviceInfo {
-  bool ok;
-  int sms;
-};
-
-// Read once per device; the calls that follow touch no device state.
-const DeviceInfo& device_info(int dev) {
-  static const struct All {
-    DeviceInfo d[64];
-    All() {
-      int n = 0;
-      if (cudaGetDeviceCount(&n) != cudaSuccess) {
-        cudaGetLastError();
-        n = 0;
-      }
-      for (int i = 0; i < 64; ++i) {
-        d[i] = {false, 0};
-        int major = 0;
-        if (i < n && cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, i) == cudaSuccess && major == 10 &&
-            cudaDeviceGetAttribute(&d[i].sms, cudaDevAttrMultiProcessorCount, i) == cudaSuccess)
-          d[i].ok = true;
-      }
-    }
-  } all;
-  static const DeviceInfo none{false, 0};
-  return dev >= 0 && dev < 64 ? all.d[dev] : none;
-}
-
 template <int kCg, int kBn, bool kNv>
 muon_status_t launch_product(const muon_fp4_matrix_t& a, const muon_fp4_matrix_t& b, ProdArgs g, int sms,
                              cudaStream_t st) {
@@ -638,8 +610,8 @@ muon_status_t muon_fp4_product(const muon_fp4_matrix_t* a, const muon_fp4_matrix
   if (conflict(reads, writes)) return MUON_ERR_ALIAS;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return MUON_ERR_CUDA;
-  const DeviceInfo& info = device_info(dev);
-  if (!info.ok) return MUON_ERR_UNSUPPORTED;
+  const int sms = device_sms(dev);
+  if (sms <= 0) return MUON_ERR_UNSUPPORTED;
   if (encode_fn() == nullptr) return MUON_ERR_CUDA;
   ProdArgs g = {};
   g.out = out;
@@ -658,11 +630,11 @@ muon_status_t muon_fp4_product(const muon_fp4_matrix_t* a, const muon_fp4_matrix
   const bool nv = a->format == MUON_FP4_NV;
   // pairs where there are enough 256 x 256 tiles for them, single CTAs below
   const int64_t pair_tiles = ((a->rows + 255) / 256) * ((b->rows + 255) / 256);
-  if (pair_tiles >= info.sms / 4)
-    return nv ? launch_product<2, 256, true>(*a, *b, g, info.sms, st)
-              : launch_product<2, 256, false>(*a, *b, g, info.sms, st);
-  return nv ? launch_product<1, 128, true>(*a, *b, g, info.sms, st)
-            : launch_product<1, 128, false>(*a, *b, g, info.sms, st);
+  if (pair_tiles >= sms / 4)
+    return nv ? launch_product<2, 256, true>(*a, *b, g, sms, st)
+              : launch_product<2, 256, false>(*a, *b, g, sms, st);
+  return nv ? launch_product<1, 128, true>(*a, *b, g, sms, st)
+            : launch_product<1, 128, false>(*a, *b, g, sms, st);
 }
 
 muon_status_t muon_fp4_get_status(void* stream) {

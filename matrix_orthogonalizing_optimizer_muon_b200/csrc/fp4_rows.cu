@@ -1,5 +1,29 @@
 // Product of a few bf16 rows with a 4-bit matrix, out[t, n] = X W^T (format:
-// fp4.cuh): the form for single tokens, bound by reading W once.
+// fp4.cuh): the form for single tokens.
+//
+// The bound is reading W once: 0.56 (NV) or 0.53 (MX) bytes a value, so per
+// SM about 44 values must be expanded and multiplied a cycle.  Multiplying on
+// the CUDA cores costs an instruction per value and row of X; here 16 rows of
+// W meet 8 rows of X in one mma.sync m16n8k16, whose cost does not grow with
+// the rows up to 8.  (tcgen05 has no kind that takes 4-bit and 16-bit
+// operands, and needs both in shared memory.)
+//
+//   W  goes to shared memory by cp.async, in steps of 128 k of a warp's 16
+//      rows, kDepth - 1 steps ahead (plain loads into registers were moved
+//      down to their use by the compiler: 36 us instead of XX for 65536 x 2048).  A code becomes an fp16 by one conversion for two.
+//      NV: times the block's scale, exactly (e2m1 x e4m3 has at most six
+//      significant bits within fp16's range).  MX: the exponent of a scale may
+//      be outside fp16's range, so the products of a block are summed from
+//      zero (its 32 values are exactly two MMAs) and scaled in fp32.
+//   X  is held in shared memory as fp16, each row times its own power of two
+//      that puts its largest magnitude into [2^14, 2^15).  A bf16 has 8
+//      significant bits, so values down to 2^-32 of the largest stay exact and
+//      smaller ones are off by at most 2^-39 of it, below the fp32 sums'
+//      rounding; the power is undone at the end.  A row's result so does not
+//      depend on the other rows.
+// Sums are fp32 in a fixed order.  KS warps split the k of a row tile where
+// there are too few row tiles to fill the GPU, and add up through shared
+// memory.
 #include "fp4.cuh"
 
 namespace {
@@ -7,8 +31,15 @@ namespace {
 using namespace muon;
 using namespace muon::fp4;
 
-constexpr int kThreadsR = 256;
-constexpr int kGroup = 8;  // rows of X per pass over W
+constexpr int kWarpsR = 8;
+constexpr int kThreadsR = 32 * kWarpsR;
+constexpr int kStepK = 128;          // k of a step: 32 codes a thread
+constexpr int kDepth = 4;            // ring of steps of a warp
+constexpr int kStepBytes = 1024 + 128;  // codes of 16 rows, then 8 bytes of scales a row
+constexpr int kMaxK = 10240;         // k of X in shared memory at a time
+constexpr int kXBudget = 164 * 1024; // bytes of it
+constexpr int kMxShift = 16;         // MX scales are taken times 2^-16, so that a sum of scaled products
+                                     // overflows only where a block scale is above 2^121
 
 struct RowsArgs {
   const __nv_bfloat16* x;
@@ -18,54 +49,356 @@ struct RowsArgs {
   void* out;
   int64_t ldx, ldo, pitch, atoms;
   int32_t t, n, k, out_dtype;
+  int32_t ks, kc, xpitch, tg;  // k split, k per pass, bytes of a row of X in shared memory, rows of X per CTA
 };
 
-template <bool kNv>
-__global__ void __launch_bounds__(kThreadsR) fp4_rows_kernel(const RowsArgs g) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreadsR / 32) + (threadIdx.x >> 5);
-  if (row >= g.n) return;
-  const float ts = kNv ? *g.ts : 1.0f;
-  const uint8_t* codes = g.data + row * g.pitch;
-  const uint8_t* scales = g.scales + (row >> 7) * g.atoms * kAtomBytes;
-  for (int t0 = 0; t0 < g.t; t0 += kGroup) {
-    float acc[kGroup];
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// eight codes to four fp16 pairs
+__device__ __forceinline__ void expand(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Two e8m0 scales (of the low two bytes) as bf16 pairs' bits: 2^-127 and NaN included.
+__device__ __forceinline__ uint32_t e8m0_pair(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// Exponent of the power of two that is taken out of a row of X with the
+// largest magnitude a (bits).  At least -126: below, the row's values are
+// multiples of 2^-133, times 2^126 multiples of 2^-7, exact in fp16 all the same.
+__device__ __forceinline__ int exponent_of(uint32_t a) {
+  return max(static_cast<int>(a >> 23) - 127 - 14, -126);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  // the rest of the 16 bytes is filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+template <bool kNv, int kNg>
+__global__ void __launch_bounds__(kThreadsR, 2) fp4_rows_kernel(const RowsArgs g) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint32_t amax[8 * kNg];  // bits of the largest finite magnitude of each row of X
+  uint8_t* rings = smem + 8 * kNg * g.xpitch;
+  float* part = reinterpret_cast<float*>(rings + kWarpsR * kDepth * kStepBytes);  // [warp][16 * 8 * kNg], k split only
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gr = lane >> 2, t4 = lane & 3;
+  const int ks = warp % g.ks, rw = warp / g.ks, per = kWarpsR / g.ks;
+  const int t0 = blockIdx.y * g.tg;
+  const int nt = min(g.tg, g.t - t0);
+  const int ngroups = (g.n + 16 * per - 1) / (16 * per);
+  const int chunks = static_cast<int>(g.pitch >> 4), atoms = static_cast<int>(g.atoms);  // of a row
+
+  uint8_t* ring = rings + warp * kDepth * kStepBytes;
+  const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+
+  // Where this lane copies from: piece t4 (32 codes) of a step of rows g and
+  // g + 8 of the row tile, and scale words (four blocks of a row): NV two a
+  // row, of atoms 2 j and 2 j + 1, MX one, of atom j.  NV: a lane reads back the
+  // pieces that it copied, [h][lane].  MX: a lane needs word t4 of all four
+  // pieces of its rows, which lie as [h][piece][row], so that the eight rows of
+  // an access meet no bank twice.  Scales lie as [h][word][row].
+  const int sh = kNv ? t4 >> 1 : t4 & 1, sword = kNv ? t4 & 1 : 0;
+  const uint32_t code_dst = ring_s + (kNv ? lane : t4 * 8 + gr) * 16;
+  const uint32_t scale_dst = ring_s + 1024 + (sh * 16 + sword * 8 + gr) * 4;
+  const uint8_t *code0 = nullptr, *code1 = nullptr, *scale = nullptr;
+  int piece_at = 0, atom_at = 0;
+  auto aim = [&](int grp, int k0) {  // at the first step of this warp
+    const int r0 = (grp * per + rw) * 16 + gr;
+    const int row0 = min(r0, g.n - 1), row1 = min(r0 + 8, g.n - 1), rs = sh ? row1 : row0;
+    const int j = k0 / kStepK + ks;
+    piece_at = 4 * j + t4;
+    atom_at = kNv ? 2 * j + sword : j;
+    code0 = g.data + static_cast<int64_t>(row0) * g.pitch + static_cast<int64_t>(piece_at) * 16;
+    code1 = g.data + static_cast<int64_t>(row1) * g.pitch + static_cast<int64_t>(piece_at) * 16;
+    scale = g.scales + (static_cast<int64_t>(rs >> 7) * g.atoms + atom_at) * kAtomBytes + atom_byte(rs, 0);
+  };
+  auto load = [&](uint32_t slot) {  // the step aimed at; then the next one
+    // past the row's end nothing is read (a size of 0) and zeros are written
+    const uint32_t nb = piece_at < chunks ? 16u : 0u;
+    cp_async16(code_dst + slot, nb ? code0 : g.data, nb);
+    cp_async16(code_dst + slot + 512, nb ? code1 : g.data, nb);
+    const uint32_t sb = atom_at < atoms ? 4u : 0u;
+    if (kNv || t4 < 2) cp_async4(scale_dst + slot, sb ? scale : g.scales, sb);
+    piece_at += 4 * g.ks;
+    code0 += 64 * g.ks;
+    code1 += 64 * g.ks;
+    atom_at += (kNv ? 2 : 1) * g.ks;
+    scale += (kNv ? 2 : 1) * kAtomBytes * g.ks;
+  };
+
+  // X of [k0, k0 + kc) as scaled fp16, zeros past the edges.  Within a step
+  // of 128 the 16-byte pieces lie in the order in which the four threads of a
+  // row take them: NV thread t4's i-th piece (8 values of its 32) at 4 i + t4,
+  // MX in order.
+  // Few rows are each spread over several warps.  Shared memory of rows that
+  // X does not have is left as it is: it reaches only their own columns of the
+  // products, which are not written.
+  auto stage = [&](int k0) {
+    const int kn = min(g.kc, g.k - k0);
+    const int pieces = (kn + kStepK - 1) / kStepK * (kStepK / 8);
+    const int wpr = nt > 4 ? 1 : nt > 2 ? 2 : nt > 1 ? 4 : 8;  // warps per row
+    const int first = warp / wpr, rstep = kWarpsR / wpr, p0 = (warp - first * wpr) * 32 + lane, pstep = wpr * 32;
+    auto piece = [&](const unsigned short* src, bool vec, int p) {
+      uint4 q = make_uint4(0u, 0u, 0u, 0u);
+      if (vec && p * 8 + 8 <= kn) {
+        q = __ldg(reinterpret_cast<const uint4*>(src) + p);
+      } else if (p * 8 < kn) {
+        uint32_t v[4];
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i) acc[i] = 0.0f;
-    for (int k0 = lane * 8; k0 < g.k; k0 += 256) {
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes + k0 / 2));
-      const int b = k0 / (kNv ? 16 : 32);
-      const uint32_t sb = __ldg(scales + static_cast<int64_t>(b >> 2) * kAtomBytes + atom_byte(static_cast<int>(row & 127), b));
-      const float s = kNv ? e4m3_value(sb) : e8m0_value(sb);
-      float v[8];
+        for (int i = 0; i < 4; ++i) {
+          const unsigned short* e = src + p * 8 + 2 * i;
+          const uint32_t lo = p * 8 + 2 * i < kn ? __ldg(e) : 0u, hi = p * 8 + 2 * i + 1 < kn ? __ldg(e + 1) : 0u;
+          v[i] = lo | (hi << 16);
+        }
+        q = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+      return q;
+    };
+    if (threadIdx.x < 8 * kNg) amax[threadIdx.x] = 0u;
+    __syncthreads();
+    for (int r = first; r < nt; r += rstep) {
+      const unsigned short* src = reinterpret_cast<const unsigned short*>(g.x) + static_cast<int64_t>(t0 + r) * g.ldx + k0;
+      const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+      uint32_t a = 0u;  // two magnitudes
+#pragma unroll 8
+      for (int p = p0; p < pieces; p += pstep) {
+        const uint4 q = piece(src, vec, p);
+        a = __vmaxu2(__vmaxu2(a, q.x & 0x7FFF7FFFu), __vmaxu2(q.y & 0x7FFF7FFFu, __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu)));
+      }
+      a = __reduce_max_sync(0xffffffffu, max(a & 0xFFFF0000u, a << 16));
+      if (a >= 0x7F800000u) {  // a NaN or an infinity: the finite values alone set the power of two
+        a = 0u;
+        for (int p = p0; p < pieces; p += pstep) {
+          const uint4 q = piece(src, vec, p);
+          const uint32_t v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = (v[i] << 16) & 0x7FFF0000u, hi = v[i] & 0x7FFF0000u;
+            a = max(a, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+          }
+        }
+        a = __reduce_max_sync(0xffffffffu, a);
+      }
+      if (lane == 0) atomicMax(&amax[r], a);
+    }
+    __syncthreads();
+    for (int r = first; r < nt; r += rstep) {
+      const unsigned short* src = reinterpret_cast<const unsigned short*>(g.x) + static_cast<int64_t>(t0 + r) * g.ldx + k0;
+      const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+      const float f = pow2(-exponent_of(amax[r]));
+      uint8_t* dst = smem + r * g.xpitch;
+#pragma unroll 4
+      for (int p = p0; p < pieces; p += pstep) {
+        const uint4 q = piece(src, vec, p);
+        const uint32_t v[4] = {q.x, q.y, q.z, q.w};
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 c = __floats2half2_rn(__uint_as_float(v[i] << 16) * f, __uint_as_float(v[i] & 0xFFFF0000u) * f);
+          h[i] = *reinterpret_cast<const uint32_t*>(&c);
+        }
+        const int at = kNv ? (p & ~15) + (p & 3) * 4 + ((p >> 2) & 3) : p;
+        *reinterpret_cast<uint4*>(dst + at * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+    }
+  };
+
+  const int npass = (g.k + g.kc - 1) / g.kc;
+  const uint8_t* xs = smem + gr * g.xpitch + t4 * 16;
+  const float ts = kNv ? *g.ts : 1.0f;
+  bool staged = false;
+  for (int grp = blockIdx.x; grp < ngroups; grp += gridDim.x) {
+    float total[kNg][4];
+#pragma unroll
+    for (int q = 0; q < kNg; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) total[q][i] = 0.0f;
+    for (int pass = 0; pass < npass; ++pass) {
+      const int k0 = pass * g.kc;
+      const int steps = (min(g.kc, g.k - k0) + kStepK - 1) / kStepK;
+      const int ni = (steps - ks + g.ks - 1) / g.ks;  // this warp's steps: ks, ks + KS, ...
+      aim(grp, k0);
+#pragma unroll
+      for (int d = 0; d < kDepth - 1; ++d) {
+        if (d < ni) load(d * kStepBytes);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+      if (npass > 1 || !staged) {  // behind the first loads of W
+        __syncthreads();
+        stage(k0);
+        __syncthreads();
+        staged = true;
+      }
+      float acc[kNg][4];
+#pragma unroll
+      for (int q = 0; q < kNg; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[q][i] = 0.0f;
+      const uint8_t* xj = xs + ks * (kStepK * 2);
+      auto step = [&](int i, int d) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");  // step i has landed
+        __syncwarp();  // for every lane, and step i - 1 has been read by every lane
+        const uint8_t* st = ring + d * kStepBytes;
+        uint32_t w[2][4], sw[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (kNv) {
+            const uint4 v = *reinterpret_cast<const uint4*>(st + h * 512 + lane * 16);
+            w[h][0] = v.x;
+            w[h][1] = v.y;
+            w[h][2] = v.z;
+            w[h][3] = v.w;
+            // blocks 2 t4 and 2 t4 + 1 of the step's eight: half a word
+            sw[h] = *reinterpret_cast<const unsigned short*>(st + 1024 + (h * 16 + (t4 >> 1) * 8 + gr) * 4 + (t4 & 1) * 2);
+          } else {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              w[h][b] = *reinterpret_cast<const uint32_t*>(st + h * 512 + b * 128 + gr * 16 + t4 * 4);
+            sw[h] = *reinterpret_cast<const uint32_t*>(st + 1024 + (h * 16 + gr) * 4);
+          }
+        }
+        if (i + kDepth - 1 < ni) load((d + kDepth - 1) % kDepth * kStepBytes);  // over step i - 1
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        uint32_t sc[2][2];
+        if (kNv) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(sw[h]), __NV_E4M3);
+            const uint32_t both = static_cast<uint32_t>(r.x) | (static_cast<uint32_t>(r.y) << 16);
+            sc[h][0] = __byte_perm(both, both, 0x1010);
+            sc[h][1] = __byte_perm(both, both, 0x3232);
+          }
+        }
+        uint32_t m0[2] = {0u, 0u}, m1[2] = {0u, 0u};
+        if (!kNv) {
+          m0[0] = e8m0_pair(sw[0]);
+          m0[1] = e8m0_pair(sw[0] >> 16);
+          m1[0] = e8m0_pair(sw[1]);
+          m1[1] = e8m0_pair(sw[1] >> 16);
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t lo[4], hi[4];  // rows g and g + 8
+          expand(w[0][b], lo);
+          expand(w[1][b], hi);
+          float s0 = 0.0f, s1 = 0.0f;
+          if (kNv) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              lo[p] = mul2(lo[p], sc[0][b >> 1]);
+              hi[p] = mul2(hi[p], sc[1][b >> 1]);
+            }
+          } else {
+            constexpr float kDown = 1.0f / (1 << kMxShift);
+            const uint32_t w0 = m0[b >> 1], w1 = m1[b >> 1];
+            s0 = __uint_as_float((b & 1) ? (w0 & 0xFFFF0000u) : (w0 << 16)) * kDown;
+            s1 = __uint_as_float((b & 1) ? (w1 & 0xFFFF0000u) : (w1 << 16)) * kDown;
+          }
+#pragma unroll
+          for (int q = 0; q < kNg; ++q) {
+            const uint4 x = *reinterpret_cast<const uint4*>(xj + q * 8 * g.xpitch + b * 64);
+            if (kNv) {
+              mma16816(acc[q], lo[0], hi[0], lo[1], hi[1], x.x, x.y);
+              mma16816(acc[q], lo[2], hi[2], lo[3], hi[3], x.z, x.w);
+            } else {
+              float d4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              mma16816(d4, lo[0], hi[0], lo[1], hi[1], x.x, x.y);
+              mma16816(d4, lo[2], hi[2], lo[3], hi[3], x.z, x.w);
+              acc[q][0] = fmaf(s0, d4[0], acc[q][0]);
+              acc[q][1] = fmaf(s0, d4[1], acc[q][1]);
+              acc[q][2] = fmaf(s1, d4[2], acc[q][2]);
+              acc[q][3] = fmaf(s1, d4[3], acc[q][3]);
+            }
+          }
+        }
+        xj += g.ks * (kStepK * 2);
+      };
+      int i = 0;
+      for (; i + kDepth <= ni; i += kDepth) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) step(i + d, d);
+      }
+#pragma unroll
+      for (int d = 0; d < kDepth - 1; ++d)
+        if (i + d < ni) step(i + d, d);
+      __syncwarp();  // the ring is read before the next pass or tile fills it
+#pragma unroll
+      for (int q = 0; q < kNg; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          total[q][i] += acc[q][i] * pow2(exponent_of(amax[8 * q + 2 * t4 + (i & 1)])) *
+                         (kNv ? 1.0f : static_cast<float>(1 << kMxShift));
+    }
+    if (g.ks > 1) {
+      // the first warp of a row tile adds the others' sums, in order
+      __syncthreads();
+      float* mine = part + warp * (128 * kNg);
+#pragma unroll
+      for (int q = 0; q < kNg; ++q)
+        *reinterpret_cast<float4*>(mine + q * 128 + lane * 4) =
+            make_float4(total[q][0], total[q][1], total[q][2], total[q][3]);
+      __syncthreads();
+      if (ks != 0) continue;
+      for (int w = 1; w < g.ks; ++w)
+#pragma unroll
+        for (int q = 0; q < kNg; ++q) {
+          const float4 v = *reinterpret_cast<const float4*>(part + (warp + w) * (128 * kNg) + q * 128 + lane * 4);
+          total[q][0] += v.x;
+          total[q][1] += v.y;
+          total[q][2] += v.z;
+          total[q][3] += v.w;
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kNg; ++q)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 p = e2m1_pair((w >> (8 * i)) & 0xFFu);
-        v[2 * i] = p.x * s;
-        v[2 * i + 1] = p.y * s;
+        const int row = (grp * per + rw) * 16 + gr + (i >> 1) * 8;
+        const int t = 8 * q + 2 * t4 + (i & 1);
+        if (row >= g.n || t >= nt) continue;
+        const float v = kNv ? total[q][i] * ts : total[q][i];
+        const int64_t at = static_cast<int64_t>(t0 + t) * g.ldo + row;
+        if (g.out_dtype == MUON_DT_BF16) static_cast<__nv_bfloat16*>(g.out)[at] = __float2bfloat16_rn(v);
+        else static_cast<float*>(g.out)[at] = v;
       }
-#pragma unroll
-      for (int t = 0; t < kGroup; ++t) {
-        if (t0 + t >= g.t) continue;
-        const __nv_bfloat16* x = g.x + (t0 + t) * g.ldx + k0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (k0 + i < g.k) acc[t] = fmaf(__bfloat162float(x[i]), v[i], acc[t]);
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < kGroup; ++t) {
-      float a = acc[t];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-      if (lane == 0 && t0 + t < g.t) {
-        a *= ts;
-        const int64_t at = (t0 + t) * g.ldo + row;
-        if (g.out_dtype == MUON_DT_BF16) static_cast<__nv_bfloat16*>(g.out)[at] = __float2bfloat16_rn(a);
-        else static_cast<float*>(g.out)[at] = a;
-      }
-    }
   }
+}
+
+template <bool kNv, int kNg>
+cudaError_t launch_rows(const RowsArgs& g, dim3 grid, int smem, cudaStream_t st) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(fp4_rows_kernel<kNv, kNg>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  fp4_rows_kernel<kNv, kNg><<<grid, kThreadsR, smem, st>>>(g);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -91,12 +424,37 @@ extern "C" muon_status_t muon_fp4_rows_product(const void* x, int64_t t, int64_t
   reads.push_back(ByteRange{xa, xa + (static_cast<size_t>(t - 1) * ldx + w->k) * 2});
   writes.push_back(ByteRange{o, o + (static_cast<size_t>(t - 1) * ldo + w->rows) * es});
   if (conflict(reads, writes)) return MUON_ERR_ALIAS;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MUON_ERR_CUDA;
+  const int sms = device_sms(dev);
+  if (sms <= 0) return MUON_ERR_UNSUPPORTED;
+
   RowsArgs g{static_cast<const __nv_bfloat16*>(x), static_cast<const uint8_t*>(w->data),
              static_cast<const uint8_t*>(w->scales), w->tensor_scale, out, ldx, ldo, pitch_of(w->k),
              atoms_of(w->format, w->k), static_cast<int32_t>(t), static_cast<int32_t>(w->rows),
-             static_cast<int32_t>(w->k), out_dtype};
-  const unsigned blocks = static_cast<unsigned>((w->rows + kThreadsR / 32 - 1) / (kThreadsR / 32));
-  if (w->format == MUON_FP4_NV) fp4_rows_kernel<true><<<blocks, kThreadsR, 0, st>>>(g);
-  else fp4_rows_kernel<false><<<blocks, kThreadsR, 0, st>>>(g);
-  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+             static_cast<int32_t>(w->k), out_dtype, 0, 0, 0, 0};
+  // k of a pass: all of it, up to what eight rows of X fit for.  Neither this
+  // nor the k split depends on t, so that a row's sums have one order.
+  g.kc = static_cast<int32_t>(w->k < kMaxK ? w->k : kMaxK);
+  // rows of X in shared memory are 64 bytes past a multiple of 128, so that the
+  // eight lanes of a 16-byte access (two rows, four pieces) meet no bank twice
+  g.xpitch = (g.kc + kStepK - 1) / kStepK * kStepK * 2 + 64;
+  int ng = t <= 8 ? 1 : t <= 16 ? 2 : 4;
+  while (ng > 1 && 8 * ng * g.xpitch > kXBudget) ng /= 2;
+  g.tg = 8 * ng;
+  const int64_t tiles = (w->rows + 15) / 16;
+  g.ks = 1;
+  while (g.ks < kWarpsR && tiles * g.ks < 2 * kWarpsR * static_cast<int64_t>(sms)) g.ks *= 2;
+  const int per = kWarpsR / g.ks;
+  const int64_t groups = (tiles + per - 1) / per;
+  const int smem = 8 * ng * g.xpitch + kWarpsR * kDepth * kStepBytes + (g.ks > 1 ? kWarpsR * 128 * ng * 4 : 0);
+  const int resident = smem <= 100 * 1024 ? 2 : 1;
+  const int64_t want = static_cast<int64_t>(sms) * resident;
+  const dim3 grid(static_cast<unsigned>(groups < want ? groups : want), static_cast<unsigned>((t + g.tg - 1) / g.tg));
+  const bool nv = w->format == MUON_FP4_NV;
+  cudaError_t e;
+  if (ng == 1) e = nv ? launch_rows<true, 1>(g, grid, smem, st) : launch_rows<false, 1>(g, grid, smem, st);
+  else if (ng == 2) e = nv ? launch_rows<true, 2>(g, grid, smem, st) : launch_rows<false, 2>(g, grid, smem, st);
+  else e = nv ? launch_rows<true, 4>(g, grid, smem, st) : launch_rows<false, 4>(g, grid, smem, st);
+  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
