@@ -38,6 +38,10 @@ from .api import _GDT
 _FMT = {"mx": L.MUON_FP4_MX, "nv": L.MUON_FP4_NV}
 _BLOCK = {"mx": 32, "nv": 16}
 MAX_ROWS = L.MUON_FP4_MAX_ROWS
+_MAX_DIM = 1 << 30
+
+
+_NOTHING = nullcontext()
 
 
 def _on(device, stream):
@@ -46,13 +50,18 @@ def _on(device, stream):
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
+    if torch._C._cuda_getDevice() != device.index:
         return torch.cuda.device(device)
-    return nullcontext()
+    return _NOTHING
 
 
 def _current(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _sizes(fmt: str, rows: int, k: int):
+    """(bytes of the codes, bytes of the scales), as muon_fp4_sizes gives them."""
+    return rows * (-(-k // 32) * 16), -(-rows // 128) * -(-k // (4 * _BLOCK[fmt])) * 512
 
 
 def _matrix_arg(t, name: str, dtypes=(torch.bfloat16, torch.float32)) -> int:
@@ -86,12 +95,14 @@ class Fp4Matrix:
     def __init__(self, rows: int, k: int, fmt: str, data: torch.Tensor, scales: torch.Tensor,
                  tensor_scale: torch.Tensor | None = None):
         _check_fmt(fmt)
-        self.rows, self.k, self.fmt = int(rows), int(k), fmt
-        _, data_bytes, scale_bytes = L.muon_fp4_sizes(_FMT[fmt], self.rows, self.k)
-        for t, name, dt, n in ((data, "data", torch.uint8, data_bytes), (scales, "scales", torch.uint8, scale_bytes),
-                               (tensor_scale, "tensor_scale", torch.float32, 2)):
-            if name == "tensor_scale" and fmt == "mx":
-                continue
+        rows, k = int(rows), int(k)
+        if rows < 0 or k < 0 or rows > _MAX_DIM or k > _MAX_DIM:
+            raise ValueError(f"a 4-bit matrix has 0 to 2^30 rows and columns, not {rows} x {k}")
+        data_bytes, scale_bytes = _sizes(fmt, rows, k)
+        parts = [(data, "data", torch.uint8, data_bytes), (scales, "scales", torch.uint8, scale_bytes)]
+        if fmt == "nv":
+            parts.append((tensor_scale, "tensor_scale", torch.float32, 2))
+        for t, name, dt, n in parts:
             if not isinstance(t, torch.Tensor) or not t.is_cuda:
                 raise TypeError(f"{name} must be a CUDA tensor")
             if t.dtype != dt:
@@ -100,25 +111,47 @@ class Fp4Matrix:
                 raise ValueError(f"{name} must be contiguous with {n} elements, got {tuple(t.shape)}")
             if t.device != data.device:
                 raise ValueError(f"{name} is on {t.device}, data on {data.device}")
-        self.data, self.scales = data, scales
-        self.tensor_scale = tensor_scale if fmt == "nv" else None
-        self._desc = L.muon_fp4_matrix_t(data.data_ptr(), scales.data_ptr(),
-                                         self.tensor_scale.data_ptr() if fmt == "nv" else None, self.rows, self.k,
-                                         _FMT[fmt], 0)
+        self._set(rows, k, fmt, data.device, data.data_ptr(), scales.data_ptr(),
+                  tensor_scale.data_ptr() if fmt == "nv" else None)
+        self._parts = data, scales, tensor_scale if fmt == "nv" else None
+
+    def _set(self, rows, k, fmt, device, data_ptr, scales_ptr, ts_ptr):
+        self.rows, self.k, self.fmt, self.device = rows, k, fmt, device
+        self._desc = L.muon_fp4_matrix_t(data_ptr, scales_ptr, ts_ptr, rows, k, _FMT[fmt], 0)
 
     @classmethod
     def empty(cls, rows: int, k: int, fmt: str = "nv", device=None) -> "Fp4Matrix":
         """Uninitialised storage in one allocation."""
         _check_fmt(fmt)
-        _, nd, ns = L.muon_fp4_sizes(_FMT[fmt], rows, k)
+        if rows < 0 or k < 0 or rows > _MAX_DIM or k > _MAX_DIM:
+            raise ValueError(f"a 4-bit matrix has 0 to 2^30 rows and columns, not {rows} x {k}")
+        nd, ns = _sizes(fmt, rows, k)
         off = -(-nd // 256) * 256
         buf = torch.empty(off + ns + 8, dtype=torch.uint8, device=device if device is not None else "cuda")
-        ts = buf[off + ns:].view(torch.float32) if fmt == "nv" else None
-        return cls(rows, k, fmt, buf[:nd], buf[off:off + ns], ts)
+        m = cls.__new__(cls)
+        at = buf.data_ptr()
+        m._set(rows, k, fmt, buf.device, at, at + off, at + off + ns if fmt == "nv" else None)
+        m._parts, m._buf = None, (buf, nd, off, ns)
+        return m
+
+    def _views(self):
+        """(codes, scales, tensor scale) as tensors; cut from the allocation when first asked for."""
+        if self._parts is None:
+            buf, nd, off, ns = self._buf
+            self._parts = buf[:nd], buf[off:off + ns], buf[off + ns:].view(torch.float32) if self.fmt == "nv" else None
+        return self._parts
 
     @property
-    def device(self):
-        return self.data.device
+    def data(self) -> torch.Tensor:
+        return self._views()[0]
+
+    @property
+    def scales(self) -> torch.Tensor:
+        return self._views()[1]
+
+    @property
+    def tensor_scale(self) -> torch.Tensor | None:
+        return self._views()[2]
 
     @property
     def shape(self):
