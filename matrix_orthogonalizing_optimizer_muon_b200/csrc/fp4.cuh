@@ -133,10 +133,28 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
   return __half2float(__half(h));
 }
 
-// Two codes (low four bits first) as their values.
-__device__ __forceinline__ float2 e2m1_pair(uint32_t byte) {
-  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
-  return __half22float2(__half2(h));
+// Eight codes (lowest four bits first) as four fp16 pairs.
+__device__ __forceinline__ void e2m1_expand8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+// Eight codes as their values times s.
+__device__ __forceinline__ void e2m1_values8(uint32_t w, float s, float* v) {
+  uint32_t h[4];
+  e2m1_expand8(w, h);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    v[2 * i] = p.x * s;
+    v[2 * i + 1] = p.y * s;
+  }
 }
 
 // Eight values to eight codes, v[0] in the lowest four bits: nearest, ties to
@@ -168,12 +186,40 @@ __host__ __device__ __forceinline__ int tensor_exponent(uint32_t amax_bits) {
 // above the bits of infinity says that the block holds a NaN or an infinity).
 struct BlockScale {
   uint32_t byte;  // the scale byte
-  float d, r;     // NV: the scale and its reciprocal (0, 0 for a zero scale)
-                  // MX: r alone, the exact reciprocal; 0 for a non-finite block
+  float d, r;     // NV: the scale and about its reciprocal (0, 0 for a zero scale)
+                  // MX: r alone, the exact reciprocal
+                  // (the codes of a block with a NaN scale do not matter)
 };
 
+// A matrix's scale and what its blocks' scales are found with.
+struct MatrixScale {
+  float g, six, sixth;  // g, 6 g and its reciprocal
+};
+
+__device__ __forceinline__ MatrixScale matrix_scale(uint32_t amax_bits) {
+  MatrixScale m;
+  m.g = __uint_as_float(static_cast<uint32_t>(tensor_exponent(amax_bits) + 127) << 23);
+  m.six = 6.0f * m.g;
+  m.sixth = __frcp_rn(m.six);
+  return m;
+}
+
+__device__ __forceinline__ float rcp_approx(float d) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return r;
+}
+
+// x / d from r, d's reciprocal to within two steps: the product is corrected
+// once by its remainder, which gives the quotient to within an fp32 rounding,
+// and exactly where it has few bits.  In this form a zero keeps its sign.
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+  const float q = x * r;
+  return fmaf(-fmaf(q, d, -x), r, q);
+}
+
 template <bool kNv>
-__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float g) {
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, const MatrixScale& m) {
   BlockScale b;
   b.d = 0.0f;
   if (kNv) {
@@ -181,37 +227,27 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float g) {
     // of one rounding: a quotient by 6 g (significand 1.5) that is not itself
     // a midpoint of e4m3 (5 significant bits) lies more than half an fp32
     // step from every midpoint.
-    const float q = __fdiv_rn(__uint_as_float(amax_bits), 6.0f * g);
-    b.byte = __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
-    b.d = e4m3_value(b.byte) * g;  // exact: four significant bits
-    b.r = b.d > 0.0f ? __frcp_rn(b.d) : 0.0f;
-    if (amax_bits >= 0x7F800000u) {
-      b.byte = 0x7Fu;
-      b.d = b.r = 0.0f;
-    }
+    const bool bad = amax_bits >= 0x7F800000u;
+    b.byte = __nv_cvt_float_to_fp8(quotient(__uint_as_float(amax_bits), m.six, m.sixth), __NV_SATFINITE, __NV_E4M3);
+    if (bad) b.byte = 0x7Fu;
+    b.d = e4m3_value(b.byte) * m.g;  // exact: four significant bits; below 2^126
+    b.r = b.byte != 0u ? rcp_approx(b.d) : 0.0f;
   } else {
     const int e = static_cast<int>(amax_bits >> 23) - 2;
     b.byte = e < 0 ? 0u : static_cast<uint32_t>(e);
     b.r = __uint_as_float((254u - b.byte) << 23);
-    if (amax_bits >= 0x7F800000u) {
-      b.byte = 255u;
-      b.r = 0.0f;
-    }
+    if (amax_bits >= 0x7F800000u) b.byte = 255u;
   }
   return b;
 }
 
 // x divided by the block's scale, such that the rounding to e2m1 that follows
 // gives the code of the exact quotient.  MX: the product with a power of two
-// is exact.  NV: the quotient by d is corrected once by its remainder, which
-// gives d's multiples exactly and the rest to within an fp32 rounding; a
-// quotient by a four-bit d that is no midpoint of e2m1 (three significant
-// bits) is more than half an fp32 step from every midpoint.
+// is exact.  NV: a quotient by a four-bit d that is no midpoint of e2m1 (three
+// significant bits) is more than half an fp32 step from every midpoint.
 template <bool kNv>
 __device__ __forceinline__ float scaled(float x, const BlockScale& b) {
-  const float q = x * b.r;
-  if (!kNv) return q;
-  return fmaf(-fmaf(q, b.d, -x), b.r, q);  // in this form a zero keeps its sign
+  return kNv ? quotient(x, b.d, b.r) : x * b.r;
 }
 
 }  // namespace fp4

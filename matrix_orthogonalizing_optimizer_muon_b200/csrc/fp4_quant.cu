@@ -3,16 +3,18 @@
 // products read after an optimizer step, and the activations and output
 // gradients of those products.
 //
-// A source [R, C] is cut into 128 x 128 tiles, one CTA each.  A thread loads
-// 16 consecutive values of a row at a time (one block of MUON_FP4_NV, half a
-// block of MUON_FP4_MX), so the form along the columns comes straight from
-// registers; for the form along the rows (the transpose, blocks down a
-// column) the tile is kept in shared memory and read back by column pairs.
-// Both forms are so written from one read of the source.  A tile holds whole
-// blocks and whole scale atoms in both directions, so no two CTAs share an
-// output byte.  MUON_FP4_NV needs the matrix's largest magnitude first: one
-// more pass over the source, whose maximum (over bits, order does not matter)
-// is kept beside the scale.
+// A source [R, C] is cut into tiles of 64 rows x 128 columns, one CTA each
+// (128 x 128 left two CTAs of fp32 tiles a SM, whose loads and column passes
+// hardly overlapped).  A thread takes 16 consecutive values of a row at a time
+// (one block of MUON_FP4_NV, half a block of MUON_FP4_MX), so the form along
+// the columns comes straight from registers; for the form along the rows (the
+// transpose, blocks down a column) the tile is kept in shared memory and read
+// back by columns.  Both forms are so written from one read of the source.  A
+// tile holds whole blocks in both directions, so no two CTAs write a byte;
+// there is an even number of tile rows, so that whole scale atoms are written.
+// MUON_FP4_NV needs the matrix's largest magnitude first: one more pass over
+// the source (the maximum of its bits, whose order does not matter).  A plan
+// takes its list in groups that stay in L2 between the two passes.
 #include "fp4.cuh"
 
 #include <new>
@@ -22,8 +24,12 @@ namespace {
 using namespace muon;
 using namespace muon::fp4;
 
-constexpr int kTile = 128;
+constexpr int kTileR = 64, kTile = 128;  // rows and columns of a tile
 constexpr int kThreads = 256;
+constexpr int64_t kGroupBytes = int64_t(56) << 20;  // source bytes of a plan's group (L2 holds 126 MB)
+
+constexpr int kStagePitch = kTileR / 2 + 8;  // a staged row of codes along the rows
+static_assert(kTileR * (kTile * 4 + 16) + kTile * kStagePitch <= 48 * 1024, "dynamic shared memory without opt-in");
 
 struct Form {
   uint8_t* data;   // codes, NULL: this form is not wanted
@@ -51,16 +57,19 @@ template <typename T>
 struct Src;
 template <>
 struct Src<__nv_bfloat16> {
+  using Raw = unsigned short;
   static constexpr int kWords = 8;                 // words of 16 values
   static constexpr int kPitch = kTile * 2 + 16;    // shared-memory row
 };
 template <>
 struct Src<float> {
+  using Raw = unsigned int;
   static constexpr int kWords = 16;
   static constexpr int kPitch = kTile * 4 + 16;
 };
 
 // 16 values of row `row` from column `col` on, as words; zeros past the edges.
+// For rows on 16-byte boundaries.
 template <typename T>
 __device__ __forceinline__ void load16(const Item& it, int row, int col, uint32_t (&w)[Src<T>::kWords]) {
   constexpr int kW = Src<T>::kWords;
@@ -70,7 +79,7 @@ __device__ __forceinline__ void load16(const Item& it, int row, int col, uint32_
     return;
   }
   const T* p = static_cast<const T*>(it.src) + static_cast<int64_t>(row) * it.ld + col;
-  if (it.vec && col + 16 <= it.cols) {
+  if (col + 16 <= it.cols) {
 #pragma unroll
     for (int i = 0; i < kW / 4; ++i) {
       const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
@@ -95,14 +104,38 @@ __device__ __forceinline__ void load16(const Item& it, int row, int col, uint32_
   }
 }
 
-// Bits (as fp32) of the largest magnitude of 16 values.
+// The tile of a source whose rows start anywhere: a warp's lanes take
+// consecutive values of a row, into the shared-memory tile.
+template <typename T>
+__device__ __forceinline__ void fill_tile(const Item& it, int row0, int col0, uint8_t* smem) {
+  using Raw = typename Src<T>::Raw;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int r = warp; r < kTileR; r += kThreads / 32) {
+    const Raw* p = static_cast<const Raw*>(it.src) + static_cast<int64_t>(row0 + r) * it.ld + col0;
+    Raw* d = reinterpret_cast<Raw*>(smem + r * Src<T>::kPitch);
+#pragma unroll
+    for (int c = 0; c < kTile; c += 32)
+      d[c + lane] = row0 + r < it.rows && col0 + c + lane < it.cols ? __ldg(p + c + lane) : Raw(0);
+  }
+}
+
+// The larger magnitude; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Bits (as fp32) of the largest magnitude of 16 values; at or above infinity's
+// bits where one is not finite.
 template <typename T>
 __device__ __forceinline__ uint32_t amax16(const uint32_t (&w)[Src<T>::kWords]) {
   if (sizeof(T) == 4) {
-    uint32_t a = 0u;
+    float a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < Src<T>::kWords; ++i) a = max(a, w[i] & 0x7FFFFFFFu);
-    return a;
+    for (int i = 0; i < Src<T>::kWords; ++i) a = max_nan(a, fabsf(__uint_as_float(w[i])));
+    return __float_as_uint(a);
   }
   uint32_t a = 0u;
 #pragma unroll
@@ -117,11 +150,13 @@ __device__ __forceinline__ float value_at(const uint32_t (&w)[Src<T>::kWords], i
   return __uint_as_float((i & 1) ? (v & 0xFFFF0000u) : (v << 16));
 }
 
-__device__ __forceinline__ float scale_of_amax(uint32_t bits) {
-  return __uint_as_float(static_cast<uint32_t>(tensor_exponent(bits) + 127) << 23);
+// ---------------------------------------------------------------- largest magnitude
+// bits, or 0 for a NaN or an infinity
+__device__ __forceinline__ uint32_t finite_bits(uint32_t w) {
+  const uint32_t m = w & 0x7FFFFFFFu;
+  return m < 0x7F800000u ? m : 0u;
 }
 
-// ---------------------------------------------------------------- largest magnitude
 template <typename T>
 __global__ void __launch_bounds__(kThreads) amax_kernel(const Item one, const Item* __restrict__ items,
                                                         const TileRef* __restrict__ tiles) {
@@ -129,24 +164,38 @@ __global__ void __launch_bounds__(kThreads) amax_kernel(const Item one, const It
   TileRef ref{0, static_cast<int32_t>(blockIdx.x)};
   if (tiles != nullptr) ref = tiles[blockIdx.x];
   const Item it = items != nullptr ? items[ref.item] : one;
-  const int row0 = ref.tile / it.tiles_x * kTile, col0 = ref.tile % it.tiles_x * kTile;
+  const int row0 = ref.tile / it.tiles_x * kTileR, col0 = ref.tile % it.tiles_x * kTile;
   uint32_t a = 0u;
-#pragma unroll 2
-  for (int u = threadIdx.x; u < kTile * 8; u += kThreads) {
-    uint32_t w[Src<T>::kWords];
-    load16<T>(it, row0 + (u >> 3), col0 + (u & 7) * 16, w);
-    if (sizeof(T) == 4) {
+  if (it.vec) {
+    constexpr int kN = kTileR * 8 / kThreads;
+    uint32_t w[kN][Src<T>::kWords];
 #pragma unroll
-      for (int i = 0; i < Src<T>::kWords; ++i) {
-        const uint32_t m = w[i] & 0x7FFFFFFFu;
-        a = max(a, m < 0x7F800000u ? m : 0u);
-      }
-    } else {
+    for (int k = 0; k < kN; ++k) {
+      const int u = threadIdx.x + k * kThreads;
+      load16<T>(it, row0 + (u >> 3), col0 + (u & 7) * 16, w[k]);
+    }
 #pragma unroll
-      for (int i = 0; i < Src<T>::kWords; ++i) {
-        const uint32_t hi = w[i] & 0x7FFF0000u, lo = (w[i] << 16) & 0x7FFF0000u;
-        a = max(a, max(hi < 0x7F800000u ? hi : 0u, lo < 0x7F800000u ? lo : 0u));
-      }
+    for (int k = 0; k < kN; ++k) a = max(a, amax16<T>(w[k]));
+    if (a >= 0x7F800000u) {  // not finite: the finite values alone
+      a = 0u;
+#pragma unroll
+      for (int k = 0; k < kN; ++k)
+#pragma unroll
+        for (int i = 0; i < Src<T>::kWords; ++i) {
+          if (sizeof(T) == 4) a = max(a, finite_bits(w[k][i]));
+          else a = max(a, max(finite_bits(w[k][i] & 0xFFFF0000u), finite_bits(w[k][i] << 16)));
+        }
+    }
+  } else {
+    using Raw = typename Src<T>::Raw;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll 4
+    for (int r = warp; r < kTileR; r += kThreads / 32) {
+      const Raw* p = static_cast<const Raw*>(it.src) + static_cast<int64_t>(row0 + r) * it.ld + col0;
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32)
+        if (row0 + r < it.rows && col0 + c + lane < it.cols)
+          a = max(a, finite_bits(static_cast<uint32_t>(__ldg(p + c + lane)) << (sizeof(T) == 4 ? 0 : 16)));
     }
   }
   a = __reduce_max_sync(0xffffffffu, a);
@@ -165,162 +214,210 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const Item one, const I
                                                          const TileRef* __restrict__ tiles) {
   constexpr int kW = Src<T>::kWords;
   constexpr int kPitch = Src<T>::kPitch;
-  constexpr int kAtoms = kNv ? 2 : 1;      // scale atoms of a tile in one direction
-  constexpr int kStage = kTile / 2 + 8;    // staged row of codes along the rows
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint8_t* stage = smem + kTile * kPitch;  // [128][kStage], rows form only
-  __shared__ __align__(16) uint8_t sc_c[1024];
-  __shared__ __align__(16) uint8_t sc_r[1024];
+  constexpr int kBlk = kNv ? 16 : 32;
+  constexpr int kAtomsC = kTile / (4 * kBlk);  // atoms of a tile along the columns (of each, the half with its 64 rows)
+  extern __shared__ __align__(16) uint8_t smem[];  // the tile: rows form, or rows that start anywhere
+  uint8_t* stage = smem + kTileR * kPitch;         // [128][kStagePitch] codes along the rows
+  __shared__ __align__(16) uint8_t sc_c[kAtomsC * 256];
+  __shared__ __align__(16) uint8_t sc_r[kAtomBytes];
   TileRef ref{0, static_cast<int32_t>(blockIdx.x)};
   if (tiles != nullptr) ref = tiles[blockIdx.x];
   const Item it = items != nullptr ? items[ref.item] : one;
   const int ty = ref.tile / it.tiles_x, tx = ref.tile % it.tiles_x;
-  const int row0 = ty * kTile, col0 = tx * kTile;
+  const int row0 = ty * kTileR, col0 = tx * kTile;
+  const int half = ty & 1;  // of the 128 rows of an atom
   const int t = threadIdx.x;
-  float g = 1.0f;
+  MatrixScale g = {};
   if (kNv) {
     const uint32_t bits = *it.amax;
-    g = scale_of_amax(bits);
+    g = matrix_scale(bits);
     if (ref.tile == 0 && t == 0) {
       if (kCols) {
-        it.c.ts[0] = g;
+        it.c.ts[0] = g.g;
         it.c.ts[1] = __uint_as_float(bits);
       }
       if (kRows) {
-        it.r.ts[0] = g;
+        it.r.ts[0] = g.g;
         it.r.ts[1] = __uint_as_float(bits);
       }
     }
   }
 
   // ---- by rows: units of 16 values, unit u = (row u / 8, columns 16 (u % 8))
-#pragma unroll 2
-  for (int k = 0; k < kTile * 8 / kThreads; ++k) {
-    const int u = t + k * kThreads;
-    const int r = u >> 3, c16 = u & 7;
-    uint32_t w[kW];
-    load16<T>(it, row0 + r, col0 + c16 * 16, w);
-    if (kRows) {
-      uint4* s = reinterpret_cast<uint4*>(smem + r * kPitch + c16 * 16 * sizeof(T));
+  constexpr int kN = kTileR * 8 / kThreads;
+  uint32_t w[kN][kW];
+  if (it.vec) {
 #pragma unroll
-      for (int i = 0; i < kW / 4; ++i) s[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    for (int k = 0; k < kN; ++k) {
+      const int u = t + k * kThreads;
+      load16<T>(it, row0 + (u >> 3), col0 + (u & 7) * 16, w[k]);
     }
+    if (kRows) {
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const int u = t + k * kThreads;
+        uint4* s = reinterpret_cast<uint4*>(smem + (u >> 3) * kPitch + (u & 7) * 16 * sizeof(T));
+#pragma unroll
+        for (int i = 0; i < kW / 4; ++i)
+          s[i] = make_uint4(w[k][4 * i], w[k][4 * i + 1], w[k][4 * i + 2], w[k][4 * i + 3]);
+      }
+    }
+  } else {
+    fill_tile<T>(it, row0, col0, smem);
+    __syncthreads();
     if (kCols) {
-      uint32_t a = amax16<T>(w);
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const int u = t + k * kThreads;
+        const uint4* s = reinterpret_cast<const uint4*>(smem + (u >> 3) * kPitch + (u & 7) * 16 * sizeof(T));
+#pragma unroll
+        for (int i = 0; i < kW / 4; ++i) {
+          const uint4 q = s[i];
+          w[k][4 * i] = q.x;
+          w[k][4 * i + 1] = q.y;
+          w[k][4 * i + 2] = q.z;
+          w[k][4 * i + 3] = q.w;
+        }
+      }
+    }
+  }
+  if (kCols) {
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const int u = t + k * kThreads;
+      const int r = u >> 3, c16 = u & 7;
+      uint32_t a = amax16<T>(w[k]);
       if (!kNv) a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
       const BlockScale bs = block_scale<kNv>(a, g);
       float v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = scaled<kNv>(value_at<T>(w, i), bs);
+      for (int i = 0; i < 16; ++i) v[i] = scaled<kNv>(value_at<T>(w[k], i), bs);
       const int64_t byte = static_cast<int64_t>(col0) / 2 + c16 * 8;
       if (row0 + r < it.rows && byte < it.c.pitch)
         *reinterpret_cast<uint2*>(it.c.data + static_cast<int64_t>(row0 + r) * it.c.pitch + byte) =
             make_uint2(e2m1_pack8(v), e2m1_pack8(v + 8));
-      if (kNv) sc_c[(c16 >> 2) * kAtomBytes + atom_byte(r, c16)] = static_cast<uint8_t>(bs.byte);
-      else if ((c16 & 1) == 0) sc_c[atom_byte(r, c16 >> 1)] = static_cast<uint8_t>(bs.byte);
+      // [atom][r % 32][r / 32][block]: the tile's half of each 16 bytes
+      const int b = kNv ? c16 : c16 >> 1;
+      if (kNv || (c16 & 1) == 0) sc_c[(b >> 2) * 256 + (r & 31) * 8 + (r >> 5) * 4 + (b & 3)] = static_cast<uint8_t>(bs.byte);
     }
   }
-  __syncthreads();
-  if (kCols && t < kAtoms * 32) {
+  if (kCols || it.vec) __syncthreads();
+  if (kCols && t < kAtomsC * 32) {
     // the tile's atoms follow each other in memory; the second may be past the last
-    const int64_t atom = static_cast<int64_t>(tx) * kAtoms + (t >> 5);
+    const int64_t atom = static_cast<int64_t>(tx) * kAtomsC + (t >> 5);
     if (atom < it.c.atoms)
-      reinterpret_cast<uint4*>(it.c.scales + (static_cast<int64_t>(ty) * it.c.atoms + atom) * kAtomBytes)[t & 31] =
-          reinterpret_cast<const uint4*>(sc_c)[t];
+      *reinterpret_cast<uint2*>(it.c.scales + (static_cast<int64_t>(ty >> 1) * it.c.atoms + atom) * kAtomBytes +
+                                (t & 31) * 16 + half * 8) = reinterpret_cast<const uint2*>(sc_c)[t];
   }
   if (!kRows) return;
 
-  // ---- by columns: unit = (column pair, block of rows)
-  constexpr int kBlk = kNv ? 16 : 32;
-  for (int u = t; u < (kTile / 2) * (kTile / kBlk); u += kThreads) {
-    const int cp = u & 63, rb = u >> 6;
-    const uint8_t* s = smem + rb * kBlk * kPitch + cp * 2 * sizeof(T);
-    uint32_t x0[kBlk], x1[kBlk];  // as fp32 bits
-    uint32_t a0 = 0u, a1 = 0u;
+  // ---- by columns: NV a thread takes two columns of one block of rows, MX one column
+  static_assert(kTile / (kNv ? 2 : 1) * (kTileR / kBlk) == kThreads, "one unit a thread");
+  {
+    constexpr int kCw = kNv ? 2 : 1;
+    const int c0 = (t % (kTile / kCw)) * kCw, rb = t / (kTile / kCw);
+    const uint8_t* s = smem + rb * kBlk * kPitch + c0 * sizeof(T);
+    uint32_t x[kCw][kBlk];  // as fp32 bits
+    uint32_t a[kCw] = {}, both = 0u;
+    float m[kCw] = {};
 #pragma unroll
     for (int i = 0; i < kBlk; ++i) {
-      if (sizeof(T) == 4) {
-        const uint2 p = *reinterpret_cast<const uint2*>(s + i * kPitch);
-        x0[i] = p.x;
-        x1[i] = p.y;
+      if constexpr (kNv) {
+        if (sizeof(T) == 4) {
+          const uint2 p = *reinterpret_cast<const uint2*>(s + i * kPitch);
+          x[0][i] = p.x;
+          x[1][i] = p.y;
+        } else {
+          const uint32_t p = *reinterpret_cast<const uint32_t*>(s + i * kPitch);
+          x[0][i] = p << 16;
+          x[1][i] = p & 0xFFFF0000u;
+          both = __vmaxu2(both, p & 0x7FFF7FFFu);
+        }
       } else {
-        const uint32_t p = *reinterpret_cast<const uint32_t*>(s + i * kPitch);
-        x0[i] = p << 16;
-        x1[i] = p & 0xFFFF0000u;
+        x[0][i] = sizeof(T) == 4 ? *reinterpret_cast<const uint32_t*>(s + i * kPitch)
+                                 : static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(s + i * kPitch)) << 16;
       }
-      a0 = max(a0, x0[i] & 0x7FFFFFFFu);
-      a1 = max(a1, x1[i] & 0x7FFFFFFFu);
+      if (sizeof(T) == 4 || !kNv) {
+#pragma unroll
+        for (int h = 0; h < kCw; ++h) m[h] = max_nan(m[h], fabsf(__uint_as_float(x[h][i])));
+      }
+    }
+    if (sizeof(T) == 2 && kNv) {
+      a[0] = both << 16;
+      a[kCw - 1] = both & 0xFFFF0000u;
+    } else {
+#pragma unroll
+      for (int h = 0; h < kCw; ++h) a[h] = __float_as_uint(m[h]);
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t* x = h ? x1 : x0;
-      const BlockScale bs = block_scale<kNv>(h ? a1 : a0, g);
-      const int c = 2 * cp + h;
-      uint8_t* out = stage + c * kStage + rb * (kBlk / 2);
+    for (int h = 0; h < kCw; ++h) {
+      const BlockScale bs = block_scale<kNv>(a[h], g);
+      const int c = c0 + h;
+      uint8_t* out = stage + c * kStagePitch + rb * (kBlk / 2);
 #pragma unroll
       for (int q = 0; q < kBlk / 16; ++q) {
         float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = scaled<kNv>(__uint_as_float(x[16 * q + i]), bs);
+        for (int i = 0; i < 16; ++i) v[i] = scaled<kNv>(__uint_as_float(x[h][16 * q + i]), bs);
         *reinterpret_cast<uint2*>(out + 8 * q) = make_uint2(e2m1_pack8(v), e2m1_pack8(v + 8));
       }
-      sc_r[(rb >> 2) * kAtomBytes + atom_byte(c, rb)] = static_cast<uint8_t>(bs.byte);
+      // NV: the atom's four blocks; MX: two of them, [c % 32][c / 32][block]
+      sc_r[(c & 31) * (kNv ? 16 : 8) + (c >> 5) * (kNv ? 4 : 2) + rb] = static_cast<uint8_t>(bs.byte);
     }
   }
   __syncthreads();
-  for (int u = t; u < kTile * 8; u += kThreads) {
-    const int c = u >> 3, q = u & 7;
+#pragma unroll
+  for (int k = 0; k < kTile * 4 / kThreads; ++k) {
+    const int u = t + k * kThreads;
+    const int c = u >> 2, q = u & 3;
     const int64_t byte = static_cast<int64_t>(row0) / 2 + q * 8;
     if (col0 + c < it.cols && byte < it.r.pitch)
       *reinterpret_cast<uint2*>(it.r.data + static_cast<int64_t>(col0 + c) * it.r.pitch + byte) =
-          *reinterpret_cast<const uint2*>(stage + c * kStage + q * 8);
+          *reinterpret_cast<const uint2*>(stage + c * kStagePitch + q * 8);
   }
-  if (t < kAtoms * 32) {
-    const int64_t atom = static_cast<int64_t>(ty) * kAtoms + (t >> 5);
-    if (atom < it.r.atoms)
-      reinterpret_cast<uint4*>(it.r.scales + (static_cast<int64_t>(tx) * it.r.atoms + atom) * kAtomBytes)[t & 31] =
+  if (kNv) {
+    if (t < 32 && ty < it.r.atoms)
+      reinterpret_cast<uint4*>(it.r.scales + (static_cast<int64_t>(tx) * it.r.atoms + ty) * kAtomBytes)[t] =
           reinterpret_cast<const uint4*>(sc_r)[t];
+  } else if (t < 128) {
+    *reinterpret_cast<unsigned short*>(it.r.scales + (static_cast<int64_t>(tx) * it.r.atoms + (ty >> 1)) * kAtomBytes +
+                                       t * 4 + half * 2) = reinterpret_cast<const unsigned short*>(sc_r)[t];
   }
 }
 
-template <typename T, bool kRows>
-constexpr int quant_smem() {
-  return kRows ? kTile * Src<T>::kPitch + kTile * (kTile / 2 + 8) : 0;
-}
+
+struct Launch {
+  const Item* one;         // a single matrix, or
+  const Item* items;       // a list
+  const TileRef* tiles;
+  int ntiles;
+  int dtype, format;
+  bool cols, rows, vec;    // vec: every source's rows start on 16-byte boundaries
+};
 
 template <typename T, bool kNv, bool kCols, bool kRows>
-cudaError_t launch_quant_t(const Item& one, const Item* items, const TileRef* tiles, int ntiles, cudaStream_t st) {
-  constexpr int smem = quant_smem<T, kRows>();
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(quant_kernel<T, kNv, kCols, kRows>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  quant_kernel<T, kNv, kCols, kRows><<<ntiles, kThreads, smem, st>>>(one, items, tiles);
+cudaError_t launch_quant_t(const Launch& l, cudaStream_t st) {
+  const int smem = (kRows || !l.vec ? kTileR * Src<T>::kPitch : 0) + (kRows ? kTile * kStagePitch : 0);
+  quant_kernel<T, kNv, kCols, kRows><<<l.ntiles, kThreads, smem, st>>>(l.one ? *l.one : Item{}, l.items, l.tiles);
   return cudaGetLastError();
 }
 
 template <typename T, bool kNv>
-cudaError_t launch_quant_n(const Item& one, const Item* items, const TileRef* tiles, int ntiles, bool cols, bool rows,
-                           cudaStream_t st) {
+cudaError_t launch_quant_n(const Launch& l, cudaStream_t st) {
   if (kNv) {
-    amax_kernel<T><<<ntiles, kThreads, 0, st>>>(one, items, tiles);
+    amax_kernel<T><<<l.ntiles, kThreads, 0, st>>>(l.one ? *l.one : Item{}, l.items, l.tiles);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (cols && rows) return launch_quant_t<T, kNv, true, true>(one, items, tiles, ntiles, st);
-  if (cols) return launch_quant_t<T, kNv, true, false>(one, items, tiles, ntiles, st);
-  return launch_quant_t<T, kNv, false, true>(one, items, tiles, ntiles, st);
+  if (l.cols && l.rows) return launch_quant_t<T, kNv, true, true>(l, st);
+  if (l.cols) return launch_quant_t<T, kNv, true, false>(l, st);
+  return launch_quant_t<T, kNv, false, true>(l, st);
 }
 
-cudaError_t launch_quant(const Item& one, const Item* items, const TileRef* tiles, int ntiles, int dtype, int format,
-                         bool cols, bool rows, cudaStream_t st) {
-  const bool nv = format == MUON_FP4_NV;
-  if (dtype == MUON_DT_BF16)
-    return nv ? launch_quant_n<__nv_bfloat16, true>(one, items, tiles, ntiles, cols, rows, st)
-              : launch_quant_n<__nv_bfloat16, false>(one, items, tiles, ntiles, cols, rows, st);
-  return nv ? launch_quant_n<float, true>(one, items, tiles, ntiles, cols, rows, st)
-            : launch_quant_n<float, false>(one, items, tiles, ntiles, cols, rows, st);
+cudaError_t launch_quant(const Launch& l, cudaStream_t st) {
+  const bool nv = l.format == MUON_FP4_NV;
+  if (l.dtype == MUON_DT_BF16) return nv ? launch_quant_n<__nv_bfloat16, true>(l, st) : launch_quant_n<__nv_bfloat16, false>(l, st);
+  return nv ? launch_quant_n<float, true>(l, st) : launch_quant_n<float, false>(l, st);
 }
 
 // ---------------------------------------------------------------- back to values
@@ -332,11 +429,11 @@ struct Deq {
   int64_t ld;      // elements
   int64_t pitch, atoms;
   int32_t rows, k;
-  int32_t vec;     // destination rows start on 16-byte boundaries
-  int32_t units;   // ceil(k / 8): units of a row
+  uint32_t units;  // of a row: ceil(k / 16), or a head and ceil(k / 8)
+  uint32_t magic;  // ceil(2^32 / units): the quotient of a small number by `units` is the high word of a product
 };
 
-constexpr int kDeqChunk = 8192;  // units (of 8 values) per CTA
+constexpr int kDeqChunk = 1024;  // units per CTA
 
 struct DeqRef {
   int32_t item;
@@ -344,14 +441,82 @@ struct DeqRef {
   int64_t first;  // first unit of the CTA
 };
 
+// The CTA's unit e of a matrix, as (row, unit of the row): first_unit + e =
+// dr units + unit with e < 2^11, so the rounded-up reciprocal is off by at most one.
+__device__ __forceinline__ void place(const Deq& it, int64_t first_row, uint32_t first_unit, int e, int64_t& row, int& unit) {
+  const uint32_t lin = first_unit + static_cast<uint32_t>(e);
+  uint32_t dr = it.units == 1u ? lin : __umulhi(lin, it.magic);
+  if (dr * it.units > lin) --dr;
+  unit = static_cast<int>(lin - dr * it.units);
+  row = first_row + dr;
+}
+
+// Eight values from `out` on, the first `len` of them.
+template <typename T>
+__device__ __forceinline__ void store_values(T* out, const float* v, int len) {
+  if (len >= 8) {
+    if (sizeof(T) == 4) {
+      reinterpret_cast<float4*>(out)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      __align__(16) __nv_bfloat162 h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(h);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < len) {
+        if (sizeof(T) == 4) reinterpret_cast<float*>(out)[i] = v[i];
+        else reinterpret_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v[i]);
+      }
+  }
+}
+
+// Rows of the destination on 16-byte boundaries: a unit is 16 values, within one block.
 template <typename T, bool kNv>
 __global__ void __launch_bounds__(kThreads) dequant_kernel(const Deq one, const Deq* __restrict__ items,
                                                            const DeqRef* __restrict__ refs) {
   DeqRef ref{0, 0, static_cast<int64_t>(blockIdx.x) * kDeqChunk};
   if (refs != nullptr) ref = refs[blockIdx.x];
   const Deq it = items != nullptr ? items[ref.item] : one;
-  const int64_t total = static_cast<int64_t>(it.rows) * it.units;
-  const int64_t left = total - ref.first;
+  const int64_t left = static_cast<int64_t>(it.rows) * it.units - ref.first;
+  const int n = static_cast<int>(left < kDeqChunk ? left : kDeqChunk);
+  const float g = kNv ? it.ts[0] : 1.0f;
+  const int64_t first_row = ref.first / it.units;
+  const uint32_t first_unit = static_cast<uint32_t>(ref.first - first_row * it.units);
+#pragma unroll 4
+  for (int e = threadIdx.x; e < n; e += kThreads) {
+    int64_t row;
+    int unit;
+    place(it, first_row, first_unit, e, row, unit);
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(it.data + row * it.pitch) + unit);
+    const int b = kNv ? unit : unit >> 1;
+    const uint32_t sb = __ldg(it.scales + ((row >> 7) * it.atoms + (b >> 2)) * kAtomBytes +
+                              atom_byte(static_cast<int>(row & 127), b));
+    const float s = kNv ? e4m3_value(sb) * g : e8m0_value(sb);
+    float v[16];
+    e2m1_values8(w.x, s, v);
+    e2m1_values8(w.y, s, v + 8);
+    T* out = static_cast<T*>(it.dst) + row * it.ld + unit * 16;
+    const int len = it.k - unit * 16;
+    store_values<T>(out, v, len);
+    if (len > 8) store_values<T>(out + 8, v + 8, len - 8);
+  }
+}
+
+// Rows of the destination that start anywhere: a row's first unit is its head
+// up to a 16-byte boundary, the units after it are eight values each, stored
+// as whole 16-byte pieces (codes are four bits, so any eight of them are a
+// funnel shift of two words).
+template <typename T, bool kNv>
+__global__ void __launch_bounds__(kThreads) dequant_any_kernel(const Deq one, const Deq* __restrict__ items,
+                                                           const DeqRef* __restrict__ refs) {
+  DeqRef ref{0, 0, static_cast<int64_t>(blockIdx.x) * kDeqChunk};
+  if (refs != nullptr) ref = refs[blockIdx.x];
+  const Deq it = items != nullptr ? items[ref.item] : one;
+  const int64_t left = static_cast<int64_t>(it.rows) * it.units - ref.first;
   const int n = static_cast<int>(left < kDeqChunk ? left : kDeqChunk);
   const float g = kNv ? it.ts[0] : 1.0f;
   // the CTA's first unit by one wide division, the rest relative to it
@@ -359,57 +524,54 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const Deq one, const 
   const uint32_t first_unit = static_cast<uint32_t>(ref.first - first_row * it.units);
 #pragma unroll 4
   for (int e = threadIdx.x; e < n; e += kThreads) {
-    const uint32_t lin = first_unit + static_cast<uint32_t>(e);
-    const uint32_t dr = lin / static_cast<uint32_t>(it.units);
-    const int unit = static_cast<int>(lin - dr * static_cast<uint32_t>(it.units));
-    const int64_t row = first_row + dr;
-    const int b = unit / (kNv ? 2 : 4);
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(it.data + row * it.pitch) + unit);
-    const uint32_t sb = __ldg(it.scales + ((row >> 7) * it.atoms + (b >> 2)) * kAtomBytes +
-                              atom_byte(static_cast<int>(row & 127), b));
-    const float s = kNv ? e4m3_value(sb) * g : e8m0_value(sb);
+    int64_t row;
+    int unit;
+    place(it, first_row, first_unit, e, row, unit);
+    T* dst = static_cast<T*>(it.dst) + row * it.ld;
+    int k0, len;
+    const int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15) / static_cast<int>(sizeof(T));
+    k0 = unit == 0 ? 0 : head + (unit - 1) * 8;
+    len = unit == 0 ? head : 8;
+    len = min(len, it.k - k0);
+    if (len <= 0) continue;
+    const uint32_t* codes = reinterpret_cast<const uint32_t*>(it.data + row * it.pitch);
+    const int wi = k0 >> 3, sh = (k0 & 7) * 4;
+    uint32_t w = __ldg(codes + wi);
+    if (sh != 0) w = __funnelshift_r(w, (wi + 1) * 4 < it.pitch ? __ldg(codes + wi + 1) : 0u, sh);
+    const uint8_t* srow = it.scales + (row >> 7) * it.atoms * kAtomBytes + atom_byte(static_cast<int>(row & 127), 0);
+    const int b0 = k0 / (kNv ? 16 : 32), b1 = (k0 + len - 1) / (kNv ? 16 : 32);
+    auto scale = [&](int b) {
+      const uint32_t sb = __ldg(srow + static_cast<int64_t>(b >> 2) * kAtomBytes + (b & 3));
+      return kNv ? e4m3_value(sb) * g : e8m0_value(sb);
+    };
+    const float s0 = scale(b0);
+    const float s1 = b1 != b0 ? scale(b1) : s0;
+    const int turn = b1 * (kNv ? 16 : 32) - k0;  // values from here on are the next block's
     float v[8];
+    e2m1_values8(w, 1.0f, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 p = e2m1_pair((w >> (8 * i)) & 0xFFu);
-      v[2 * i] = p.x * s;
-      v[2 * i + 1] = p.y * s;
-    }
-    const int k0 = unit * 8;
-    T* out = static_cast<T*>(it.dst) + row * it.ld + k0;
-    if (it.vec && k0 + 8 <= it.k) {
-      if (sizeof(T) == 4) {
-        reinterpret_cast<float4*>(out)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
-        __align__(16) __nv_bfloat162 h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(h);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (k0 + i < it.k) {
-          if (sizeof(T) == 4) reinterpret_cast<float*>(out)[i] = v[i];
-          else reinterpret_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v[i]);
-        }
-    }
+    for (int i = 0; i < 8; ++i) v[i] *= i < turn ? s0 : s1;
+    store_values<T>(dst + k0, v, len);
   }
 }
 
-cudaError_t launch_dequant(const Deq& one, const Deq* items, const DeqRef* refs, int64_t nblocks, int dtype, int format,
-                           cudaStream_t st) {
+template <typename T, bool kNv>
+cudaError_t launch_dequant_t(const Deq& one, const Deq* items, const DeqRef* refs, int64_t nblocks, bool vec,
+                             cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(nblocks));
-  const bool nv = format == MUON_FP4_NV;
-  if (dtype == MUON_DT_BF16) {
-    if (nv) dequant_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, st>>>(one, items, refs);
-    else dequant_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, st>>>(one, items, refs);
-  } else {
-    if (nv) dequant_kernel<float, true><<<grid, kThreads, 0, st>>>(one, items, refs);
-    else dequant_kernel<float, false><<<grid, kThreads, 0, st>>>(one, items, refs);
-  }
+  if (vec) dequant_kernel<T, kNv><<<grid, kThreads, 0, st>>>(one, items, refs);
+  else dequant_any_kernel<T, kNv><<<grid, kThreads, 0, st>>>(one, items, refs);
   return cudaGetLastError();
+}
+
+cudaError_t launch_dequant(const Deq& one, const Deq* items, const DeqRef* refs, int64_t nblocks, int dtype, int format,
+                           bool vec, cudaStream_t st) {
+  const bool nv = format == MUON_FP4_NV;
+  if (dtype == MUON_DT_BF16)
+    return nv ? launch_dequant_t<__nv_bfloat16, true>(one, items, refs, nblocks, vec, st)
+              : launch_dequant_t<__nv_bfloat16, false>(one, items, refs, nblocks, vec, st);
+  return nv ? launch_dequant_t<float, true>(one, items, refs, nblocks, vec, st)
+            : launch_dequant_t<float, false>(one, items, refs, nblocks, vec, st);
 }
 
 // ---------------------------------------------------------------- host checks
@@ -438,7 +600,7 @@ muon_status_t make_item(const muon_fp4_source_t& s, Item& it, bool& empty) {
   const int es = size_of(s.src_dtype);
   const uintptr_t a = reinterpret_cast<uintptr_t>(s.src);
   if (a % es != 0) return MUON_ERR_INVALID_ARG;
-  const int64_t tx = (s.cols + kTile - 1) / kTile, ty = (s.rows + kTile - 1) / kTile;
+  const int64_t tx = (s.cols + kTile - 1) / kTile, ty = (s.rows + kAtomRows - 1) / kAtomRows * (kAtomRows / kTileR);
   if (tx * ty > 0x7fffffff) return MUON_ERR_UNSUPPORTED;
   it = Item{};
   it.src = s.src;
@@ -457,7 +619,9 @@ muon_status_t make_item(const muon_fp4_source_t& s, Item& it, bool& empty) {
   return MUON_OK;
 }
 
-int tiles_of(const Item& it) { return it.tiles_x * ((it.rows + kTile - 1) / kTile); }
+int tiles_of(const Item& it) {
+  return it.tiles_x * ((it.rows + kAtomRows - 1) / kAtomRows * (kAtomRows / kTileR));
+}
 
 template <class List>
 void item_ranges(const muon_fp4_source_t& s, List& reads, List& writes) {
@@ -466,13 +630,19 @@ void item_ranges(const muon_fp4_source_t& s, List& reads, List& writes) {
   if (s.along_rows.format >= 0) add_ranges(s.along_rows, writes);
 }
 
-muon_status_t make_deq(const muon_fp4_matrix_t& m, void* dst, int64_t ld, int32_t dtype, Deq& d) {
+// destination rows start on 16-byte boundaries
+bool deq_vec(const void* dst, int64_t ld, int32_t dtype) {
+  return reinterpret_cast<uintptr_t>(dst) % 16 == 0 && ld * size_of(dtype) % 16 == 0;
+}
+
+muon_status_t make_deq(const muon_fp4_matrix_t& m, void* dst, int64_t ld, int32_t dtype, bool vec, Deq& d) {
   if (dst == nullptr || ld < m.k || ld > (int64_t(1) << 40)) return MUON_ERR_INVALID_ARG;
   const uintptr_t a = reinterpret_cast<uintptr_t>(dst);
   if (a % size_of(dtype) != 0) return MUON_ERR_INVALID_ARG;
+  const uint32_t units = vec ? static_cast<uint32_t>((m.k + 15) / 16) : static_cast<uint32_t>((m.k + 7) / 8) + 1u;
   d = Deq{static_cast<const uint8_t*>(m.data), static_cast<const uint8_t*>(m.scales), m.tensor_scale, dst, ld,
-          pitch_of(m.k), atoms_of(m.format, m.k), static_cast<int32_t>(m.rows), static_cast<int32_t>(m.k),
-          (a % 16 == 0 && ld * size_of(dtype) % 16 == 0) ? 1 : 0, static_cast<int32_t>((m.k + 7) / 8)};
+          pitch_of(m.k), atoms_of(m.format, m.k), static_cast<int32_t>(m.rows), static_cast<int32_t>(m.k), units,
+          static_cast<uint32_t>(((uint64_t(1) << 32) + units - 1) / units)};
   return MUON_OK;
 }
 
@@ -485,9 +655,10 @@ int64_t deq_blocks(const Deq& d) {
 struct muon_fp4_plan_s {
   int device = 0;
   int dtype = 0, format = 0, values_dtype = -1;
-  bool cols = false, rows = false;
-  int ntiles = 0, nitems = 0;
-  int64_t ndeq = 0;
+  bool cols = false, rows = false, vec = true;
+  int nitems = 0, ngroups = 0;
+  int* groups = nullptr;  // host: first tile of each group, then the number of tiles
+  int64_t ndeq = 0, ndeq_vec = 0;
   uint8_t* dmem = nullptr;
   Item* items_d = nullptr;
   TileRef* tiles_d = nullptr;
@@ -528,16 +699,16 @@ muon_status_t muon_fp4_quantize(const muon_fp4_source_t* src, void* stream) {
       return MUON_ERR_CUDA;
     }
   }
-  return launch_quant(it, nullptr, nullptr, tiles_of(it), src->src_dtype, format, c, r, st) == cudaSuccess
-             ? MUON_OK
-             : MUON_ERR_CUDA;
+  const Launch l{&it, nullptr, nullptr, tiles_of(it), src->src_dtype, format, c, r, it.vec != 0};
+  return launch_quant(l, st) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
 muon_status_t muon_fp4_dequantize(const muon_fp4_matrix_t* m, void* dst, int64_t ld, int32_t dst_dtype, void* stream) {
   if (m == nullptr || !valid(*m) || !valid_dtype(dst_dtype)) return MUON_ERR_INVALID_ARG;
   if (m->rows == 0 || m->k == 0) return MUON_OK;
   Deq d;
-  const muon_status_t s = make_deq(*m, dst, ld, dst_dtype, d);
+  const bool vec = deq_vec(dst, ld, dst_dtype);
+  const muon_status_t s = make_deq(*m, dst, ld, dst_dtype, vec, d);
   if (s != MUON_OK) return s;
   RangeList reads, writes;
   writes.push_back(matrix_range(dst, m->rows, m->k, ld, dst_dtype));
@@ -545,7 +716,7 @@ muon_status_t muon_fp4_dequantize(const muon_fp4_matrix_t* m, void* dst, int64_t
   if (conflict(reads, writes)) return MUON_ERR_ALIAS;
   const int64_t nb = deq_blocks(d);
   if (nb > 0x7fffffff) return MUON_ERR_UNSUPPORTED;
-  return launch_dequant(d, nullptr, nullptr, nb, dst_dtype, m->format, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_dequant(d, nullptr, nullptr, nb, dst_dtype, m->format, vec, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MUON_OK
              : MUON_ERR_CUDA;
 }
@@ -561,8 +732,12 @@ muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs,
     std::vector<Item> items;
     std::vector<TileRef> tiles;
     std::vector<Deq> deqs;
-    std::vector<DeqRef> refs;
+    std::vector<DeqRef> refs;      // vector kernel first, then the others
+    std::vector<DeqRef> refs_any;
     std::vector<ByteRange> reads, writes;
+    std::vector<int> groups;
+    int64_t group_bytes = kGroupBytes;
+    bool vec = true;
     const bool c = srcs[0].along_cols.format >= 0, r = srcs[0].along_rows.format >= 0;
     const int32_t format = c ? srcs[0].along_cols.format : srcs[0].along_rows.format;
     for (int32_t i = 0; i < n; ++i) {
@@ -581,6 +756,14 @@ muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs,
       items.push_back(it);
       const int nt = tiles_of(it);
       if (static_cast<int64_t>(tiles.size()) + nt > 0x7fffffff) return MUON_ERR_UNSUPPORTED;
+      vec = vec && it.vec;
+      // MX needs no second pass: one group
+      const int64_t bytes = s.rows * s.cols * size_of(s.src_dtype);
+      if (tiles.empty() || (format == MUON_FP4_NV && group_bytes + bytes > kGroupBytes)) {
+        groups.push_back(static_cast<int>(tiles.size()));
+        group_bytes = 0;
+      }
+      group_bytes += bytes;
       for (int k = 0; k < nt; ++k) tiles.push_back(TileRef{id, k});
       if (values_dtype >= 0)
         for (int f = 0; f < 2; ++f) {
@@ -589,15 +772,18 @@ muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs,
           void* dst = f == 0 ? s.values_cols : s.values_rows;
           if (dst == nullptr) return MUON_ERR_INVALID_ARG;
           Deq d;
-          const muon_status_t e2 = make_deq(m, dst, m.k, values_dtype, d);
+          const bool dv = deq_vec(dst, m.k, values_dtype);
+          const muon_status_t e2 = make_deq(m, dst, m.k, values_dtype, dv, d);
           if (e2 != MUON_OK) return e2;
           writes.push_back(matrix_range(dst, m.rows, m.k, m.k, values_dtype));
           const int32_t did = static_cast<int32_t>(deqs.size());
           deqs.push_back(d);
-          for (int64_t b = 0; b < deq_blocks(d); ++b) refs.push_back(DeqRef{did, 0, b * kDeqChunk});
+          for (int64_t b = 0; b < deq_blocks(d); ++b) (dv ? refs : refs_any).push_back(DeqRef{did, 0, b * kDeqChunk});
         }
     }
     if (conflict(reads, writes)) return MUON_ERR_ALIAS;
+    const int64_t ndeq_vec = static_cast<int64_t>(refs.size());
+    refs.insert(refs.end(), refs_any.begin(), refs_any.end());
     if (refs.size() > static_cast<size_t>(0x7fffffff)) return MUON_ERR_UNSUPPORTED;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MUON_ERR_CUDA;
@@ -610,8 +796,17 @@ muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs,
     pl->cols = c;
     pl->rows = r;
     pl->nitems = static_cast<int>(items.size());
-    pl->ntiles = static_cast<int>(tiles.size());
+    pl->vec = vec;
+    pl->ngroups = static_cast<int>(groups.size());
+    groups.push_back(static_cast<int>(tiles.size()));
+    pl->groups = new (std::nothrow) int[groups.size()];
+    if (pl->groups == nullptr) {
+      delete pl;
+      return MUON_ERR_NO_MEMORY;
+    }
+    std::copy(groups.begin(), groups.end(), pl->groups);
     pl->ndeq = static_cast<int64_t>(refs.size());
+    pl->ndeq_vec = ndeq_vec;
     pl->last_stream = static_cast<cudaStream_t>(stream);
     if (!items.empty()) {
       auto up = [](size_t b) { return (b + 255) / 256 * 256; };
@@ -620,6 +815,7 @@ muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs,
                    br = up(refs.size() * sizeof(DeqRef));
       if (cudaMalloc(&pl->dmem, bi + bt + ba + bd + br) != cudaSuccess) {
         cudaGetLastError();
+        delete[] pl->groups;
         delete pl;
         return MUON_ERR_NO_MEMORY;
       }
@@ -638,6 +834,7 @@ muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs,
           !put(pl->refs_d, refs.data(), refs.size() * sizeof(DeqRef))) {
         cudaGetLastError();
         cudaFree(pl->dmem);
+        delete[] pl->groups;
         delete pl;
         return MUON_ERR_CUDA;
       }
@@ -660,10 +857,13 @@ muon_status_t muon_fp4_run(muon_fp4_plan_t pl, void* stream) {
     cudaGetLastError();
     return MUON_ERR_CUDA;
   }
-  return launch_quant(Item{}, pl->items_d, pl->tiles_d, pl->ntiles, pl->dtype, pl->format, pl->cols, pl->rows, st) ==
-                 cudaSuccess
-             ? MUON_OK
-             : MUON_ERR_CUDA;
+  for (int k = 0; k < pl->ngroups; ++k) {
+    const int first = pl->groups[k], last = pl->groups[k + 1];
+    const Launch l{nullptr, pl->items_d, pl->tiles_d + first, last - first, pl->dtype, pl->format, pl->cols, pl->rows,
+                   pl->vec};
+    if (launch_quant(l, st) != cudaSuccess) return MUON_ERR_CUDA;
+  }
+  return MUON_OK;
 }
 
 muon_status_t muon_fp4_values(muon_fp4_plan_t pl, void* stream) {
@@ -672,10 +872,13 @@ muon_status_t muon_fp4_values(muon_fp4_plan_t pl, void* stream) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev != pl->device) return MUON_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   pl->last_stream = st;
-  if (pl->ndeq == 0) return MUON_OK;
-  return launch_dequant(Deq{}, pl->deqs_d, pl->refs_d, pl->ndeq, pl->values_dtype, pl->format, st) == cudaSuccess
-             ? MUON_OK
-             : MUON_ERR_CUDA;
+  cudaError_t e = cudaSuccess;
+  if (pl->ndeq_vec > 0)
+    e = launch_dequant(Deq{}, pl->deqs_d, pl->refs_d, pl->ndeq_vec, pl->values_dtype, pl->format, true, st);
+  if (e == cudaSuccess && pl->ndeq > pl->ndeq_vec)
+    e = launch_dequant(Deq{}, pl->deqs_d, pl->refs_d + pl->ndeq_vec, pl->ndeq - pl->ndeq_vec, pl->values_dtype,
+                       pl->format, false, st);
+  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
 void muon_fp4_destroy(muon_fp4_plan_t pl) {
@@ -683,6 +886,7 @@ void muon_fp4_destroy(muon_fp4_plan_t pl) {
   cudaStreamSynchronize(pl->last_stream);
   cudaGetLastError();
   cudaFree(pl->dmem);
+  delete[] pl->groups;
   delete pl;
 }
 

@@ -60,18 +60,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// eight codes to four fp16 pairs
-__device__ __forceinline__ void expand(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -305,8 +293,8 @@ __global__ void __launch_bounds__(kThreadsR, 2) fp4_rows_kernel(const RowsArgs g
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           uint32_t lo[4], hi[4];  // rows g and g + 8
-          expand(w[0][b], lo);
-          expand(w[1][b], hi);
+          e2m1_expand8(w[0][b], lo);
+          e2m1_expand8(w[1][b], hi);
           float s0 = 0.0f, s1 = 0.0f;
           if (kNv) {
 #pragma unroll
