@@ -13,8 +13,14 @@
 // tile holds whole blocks in both directions, so no two CTAs write a byte;
 // there is an even number of tile rows, so that whole scale atoms are written.
 // MUON_FP4_NV needs the matrix's largest magnitude first: one more pass over
-// the source (the maximum of its bits, whose order does not matter).  A plan
-// takes its list in groups that stay in L2 between the two passes.
+// the source (the maximum of its bits, whose order does not matter).  (Running
+// a list in groups that stay in L2 between the passes was slower for every
+// group size: 24 fp32 matrices of 2048 x 1408, both forms, 155 us in one piece,
+// 173 to 221 us in groups of 100 to 24 MB, whose launches do not fill the GPU.)
+// Both kernels are bound by the instructions they issue, so the set-up of a
+// thread counts as much as its 32 values: a single matrix is described by
+// kernel parameters, a list by tables, in kernels of their own, and tiles
+// inside the matrix load and store without looking at its edges.
 #include "fp4.cuh"
 
 #include <new>
@@ -26,10 +32,9 @@ using namespace muon::fp4;
 
 constexpr int kTileR = 64, kTile = 128;  // rows and columns of a tile
 constexpr int kThreads = 256;
-constexpr int64_t kGroupBytes = int64_t(56) << 20;  // source bytes of a plan's group (L2 holds 126 MB)
 
 constexpr int kStagePitch = kTileR / 2 + 8;  // a staged row of codes along the rows
-static_assert(kTileR * (kTile * 4 + 16) + kTile * kStagePitch <= 48 * 1024, "dynamic shared memory without opt-in");
+static_assert(kTileR * kTile * 4 + kTile * kStagePitch <= 48 * 1024, "dynamic shared memory without opt-in");
 
 struct Form {
   uint8_t* data;   // codes, NULL: this form is not wanted
@@ -43,15 +48,23 @@ struct Item {
   const void* src;
   int64_t ld;      // elements
   int32_t rows, cols;
-  int32_t tiles_x; // tiles of 128 columns
+  int32_t tiles_x, tiles_y;  // tiles of 128 columns and 64 rows, the latter an even number
   int32_t vec;     // rows start on 16-byte boundaries
   unsigned* amax;  // NV: bits of the largest finite magnitude
   Form c, r;       // along the columns [rows, cols], along the rows [cols, rows]
 };
 
 struct TileRef {
-  int32_t item, tile;
+  int32_t item, tx, ty;
 };
+
+constexpr int kGridY = 32768;  // tile rows of a single matrix along the grid's y, the rest along z
+
+template <bool kList>
+__device__ __forceinline__ TileRef my_tile(const TileRef* __restrict__ tiles) {
+  if constexpr (kList) return tiles[blockIdx.x];
+  else return TileRef{0, static_cast<int32_t>(blockIdx.x), static_cast<int32_t>(blockIdx.z * kGridY + blockIdx.y)};
+}
 
 template <typename T>
 struct Src;
@@ -59,19 +72,41 @@ template <>
 struct Src<__nv_bfloat16> {
   using Raw = unsigned short;
   static constexpr int kWords = 8;                 // words of 16 values
-  static constexpr int kPitch = kTile * 2 + 16;    // shared-memory row
+  static constexpr int kPitch = kTile * 2;         // shared-memory row
 };
 template <>
 struct Src<float> {
   using Raw = unsigned int;
   static constexpr int kWords = 16;
-  static constexpr int kPitch = kTile * 4 + 16;
+  static constexpr int kPitch = kTile * 4;
 };
 
-// 16 values of row `row` from column `col` on, as words; zeros past the edges.
-// For rows on 16-byte boundaries.
+// Where 16-byte piece j of a row lies in the shared-memory tile.  The pieces of
+// each 128 bytes are permuted: a thread stores the pieces of its 16 values one
+// by one, and without this the eight threads of a row would meet the same
+// banks (64 or 32 bytes apart); a warp that reads 128 bytes of a row meets
+// every bank once either way.
 template <typename T>
-__device__ __forceinline__ void load16(const Item& it, int row, int col, uint32_t (&w)[Src<T>::kWords]) {
+__device__ __forceinline__ int swizzled(int j) {
+  return j ^ ((j >> 3) & (sizeof(T) == 4 ? 3 : 1));
+}
+
+// 16 values on a 16-byte boundary, as words.
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, uint32_t (&w)[Src<T>::kWords]) {
+#pragma unroll
+  for (int i = 0; i < Src<T>::kWords / 4; ++i) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    w[4 * i] = q.x;
+    w[4 * i + 1] = q.y;
+    w[4 * i + 2] = q.z;
+    w[4 * i + 3] = q.w;
+  }
+}
+
+// 16 values of row `row` from column `col` on; zeros past the edges.
+template <typename T>
+__device__ __forceinline__ void load16_edge(const Item& it, int row, int col, uint32_t (&w)[Src<T>::kWords]) {
   constexpr int kW = Src<T>::kWords;
   if (row >= it.rows || col >= it.cols) {
 #pragma unroll
@@ -80,14 +115,7 @@ __device__ __forceinline__ void load16(const Item& it, int row, int col, uint32_
   }
   const T* p = static_cast<const T*>(it.src) + static_cast<int64_t>(row) * it.ld + col;
   if (col + 16 <= it.cols) {
-#pragma unroll
-    for (int i = 0; i < kW / 4; ++i) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
-      w[4 * i] = q.x;
-      w[4 * i + 1] = q.y;
-      w[4 * i + 2] = q.z;
-      w[4 * i + 3] = q.w;
-    }
+    load16<T>(p, w);
     return;
   }
   const int left = it.cols - col;
@@ -104,6 +132,22 @@ __device__ __forceinline__ void load16(const Item& it, int row, int col, uint32_
   }
 }
 
+// This thread's units of a tile: unit k is row t / 8 + 32 k, columns 16 (t % 8) on.
+constexpr int kUnits = kTileR * 8 / kThreads;
+template <typename T>
+__device__ __forceinline__ void load_units(const Item& it, int row0, int col0, bool inside,
+                                           uint32_t (&w)[kUnits][Src<T>::kWords]) {
+  const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 16;
+  if (inside) {
+    const T* p = static_cast<const T*>(it.src) + static_cast<int64_t>(row0 + r) * it.ld + (col0 + c);
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) load16<T>(p + static_cast<int64_t>(k * (kThreads / 8)) * it.ld, w[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) load16_edge<T>(it, row0 + r + k * (kThreads / 8), col0 + c, w[k]);
+  }
+}
+
 // The tile of a source whose rows start anywhere: a warp's lanes take
 // consecutive values of a row, into the shared-memory tile.
 template <typename T>
@@ -113,10 +157,12 @@ __device__ __forceinline__ void fill_tile(const Item& it, int row0, int col0, ui
 #pragma unroll 4
   for (int r = warp; r < kTileR; r += kThreads / 32) {
     const Raw* p = static_cast<const Raw*>(it.src) + static_cast<int64_t>(row0 + r) * it.ld + col0;
-    Raw* d = reinterpret_cast<Raw*>(smem + r * Src<T>::kPitch);
+    constexpr int kPiece = 16 / sizeof(T);
 #pragma unroll
-    for (int c = 0; c < kTile; c += 32)
-      d[c + lane] = row0 + r < it.rows && col0 + c + lane < it.cols ? __ldg(p + c + lane) : Raw(0);
+    for (int c = 0; c < kTile; c += 32) {
+      Raw* d = reinterpret_cast<Raw*>(smem + r * Src<T>::kPitch + swizzled<T>((c + lane) / kPiece) * 16);
+      d[lane % kPiece] = row0 + r < it.rows && col0 + c + lane < it.cols ? __ldg(p + c + lane) : Raw(0);
+    }
   }
 }
 
@@ -157,29 +203,26 @@ __device__ __forceinline__ uint32_t finite_bits(uint32_t w) {
   return m < 0x7F800000u ? m : 0u;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) amax_kernel(const Item one, const Item* __restrict__ items,
+template <typename T, bool kList>
+__global__ void __launch_bounds__(kThreads) amax_kernel(const __grid_constant__ Item one, const Item* __restrict__ items,
                                                         const TileRef* __restrict__ tiles) {
   __shared__ uint32_t part[kThreads / 32];
-  TileRef ref{0, static_cast<int32_t>(blockIdx.x)};
-  if (tiles != nullptr) ref = tiles[blockIdx.x];
-  const Item it = items != nullptr ? items[ref.item] : one;
-  const int row0 = ref.tile / it.tiles_x * kTileR, col0 = ref.tile % it.tiles_x * kTile;
+  const TileRef ref = my_tile<kList>(tiles);
+  Item listed;
+  if constexpr (kList) listed = items[ref.item];  // all of it at once
+  const Item& it = kList ? listed : one;
+  const int row0 = ref.ty * kTileR, col0 = ref.tx * kTile;
+  if (row0 >= it.rows) return;  // the tiles that only fill up scale atoms
   uint32_t a = 0u;
   if (it.vec) {
-    constexpr int kN = kTileR * 8 / kThreads;
-    uint32_t w[kN][Src<T>::kWords];
+    uint32_t w[kUnits][Src<T>::kWords];
+    load_units<T>(it, row0, col0, row0 + kTileR <= it.rows && col0 + kTile <= it.cols, w);
 #pragma unroll
-    for (int k = 0; k < kN; ++k) {
-      const int u = threadIdx.x + k * kThreads;
-      load16<T>(it, row0 + (u >> 3), col0 + (u & 7) * 16, w[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kN; ++k) a = max(a, amax16<T>(w[k]));
+    for (int k = 0; k < kUnits; ++k) a = max(a, amax16<T>(w[k]));
     if (a >= 0x7F800000u) {  // not finite: the finite values alone
       a = 0u;
 #pragma unroll
-      for (int k = 0; k < kN; ++k)
+      for (int k = 0; k < kUnits; ++k)
 #pragma unroll
         for (int i = 0; i < Src<T>::kWords; ++i) {
           if (sizeof(T) == 4) a = max(a, finite_bits(w[k][i]));
@@ -209,8 +252,9 @@ __global__ void __launch_bounds__(kThreads) amax_kernel(const Item one, const It
 }
 
 // ---------------------------------------------------------------- quantisation
-template <typename T, bool kNv, bool kCols, bool kRows>
-__global__ void __launch_bounds__(kThreads) quant_kernel(const Item one, const Item* __restrict__ items,
+template <typename T, bool kNv, bool kCols, bool kRows, bool kList>
+__global__ void __launch_bounds__(kThreads) quant_kernel(const __grid_constant__ Item one,
+                                                         const Item* __restrict__ items,
                                                          const TileRef* __restrict__ tiles) {
   constexpr int kW = Src<T>::kWords;
   constexpr int kPitch = Src<T>::kPitch;
@@ -220,18 +264,21 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const Item one, const I
   uint8_t* stage = smem + kTileR * kPitch;         // [128][kStagePitch] codes along the rows
   __shared__ __align__(16) uint8_t sc_c[kAtomsC * 256];
   __shared__ __align__(16) uint8_t sc_r[kAtomBytes];
-  TileRef ref{0, static_cast<int32_t>(blockIdx.x)};
-  if (tiles != nullptr) ref = tiles[blockIdx.x];
-  const Item it = items != nullptr ? items[ref.item] : one;
-  const int ty = ref.tile / it.tiles_x, tx = ref.tile % it.tiles_x;
+  const TileRef ref = my_tile<kList>(tiles);
+  Item listed;
+  if constexpr (kList) listed = items[ref.item];  // all of it at once
+  const Item& it = kList ? listed : one;
+  const int ty = ref.ty, tx = ref.tx;
+  if (!kList && ty >= it.tiles_y) return;
   const int row0 = ty * kTileR, col0 = tx * kTile;
+  const bool inside = row0 + kTileR <= it.rows && col0 + kTile <= it.cols;
   const int half = ty & 1;  // of the 128 rows of an atom
   const int t = threadIdx.x;
   MatrixScale g = {};
   if (kNv) {
     const uint32_t bits = *it.amax;
     g = matrix_scale(bits);
-    if (ref.tile == 0 && t == 0) {
+    if ((tx | ty | t) == 0) {
       if (kCols) {
         it.c.ts[0] = g.g;
         it.c.ts[1] = __uint_as_float(bits);
@@ -244,22 +291,17 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const Item one, const I
   }
 
   // ---- by rows: units of 16 values, unit u = (row u / 8, columns 16 (u % 8))
-  constexpr int kN = kTileR * 8 / kThreads;
+  constexpr int kN = kUnits;
   uint32_t w[kN][kW];
   if (it.vec) {
-#pragma unroll
-    for (int k = 0; k < kN; ++k) {
-      const int u = t + k * kThreads;
-      load16<T>(it, row0 + (u >> 3), col0 + (u & 7) * 16, w[k]);
-    }
+    load_units<T>(it, row0, col0, inside, w);
     if (kRows) {
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
-        const int u = t + k * kThreads;
-        uint4* s = reinterpret_cast<uint4*>(smem + (u >> 3) * kPitch + (u & 7) * 16 * sizeof(T));
+        uint4* s = reinterpret_cast<uint4*>(smem + ((t >> 3) + k * (kThreads / 8)) * kPitch);
 #pragma unroll
         for (int i = 0; i < kW / 4; ++i)
-          s[i] = make_uint4(w[k][4 * i], w[k][4 * i + 1], w[k][4 * i + 2], w[k][4 * i + 3]);
+          s[swizzled<T>((t & 7) * (kW / 4) + i)] = make_uint4(w[k][4 * i], w[k][4 * i + 1], w[k][4 * i + 2], w[k][4 * i + 3]);
       }
     }
   } else {
@@ -268,11 +310,10 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const Item one, const I
     if (kCols) {
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
-        const int u = t + k * kThreads;
-        const uint4* s = reinterpret_cast<const uint4*>(smem + (u >> 3) * kPitch + (u & 7) * 16 * sizeof(T));
+        const uint4* s = reinterpret_cast<const uint4*>(smem + ((t >> 3) + k * (kThreads / 8)) * kPitch);
 #pragma unroll
         for (int i = 0; i < kW / 4; ++i) {
-          const uint4 q = s[i];
+          const uint4 q = s[swizzled<T>((t & 7) * (kW / 4) + i)];
           w[k][4 * i] = q.x;
           w[k][4 * i + 1] = q.y;
           w[k][4 * i + 2] = q.z;
@@ -282,19 +323,20 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const Item one, const I
     }
   }
   if (kCols) {
+    const int c16 = t & 7;
+    const int64_t byte = static_cast<int64_t>(col0) / 2 + c16 * 8;
+    uint8_t* out = it.c.data + static_cast<int64_t>(row0 + (t >> 3)) * it.c.pitch + byte;
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      const int u = t + k * kThreads;
-      const int r = u >> 3, c16 = u & 7;
+      const int r = (t >> 3) + k * (kThreads / 8);
       uint32_t a = amax16<T>(w[k]);
       if (!kNv) a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
       const BlockScale bs = block_scale<kNv>(a, g);
       float v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = scaled<kNv>(value_at<T>(w[k], i), bs);
-      const int64_t byte = static_cast<int64_t>(col0) / 2 + c16 * 8;
-      if (row0 + r < it.rows && byte < it.c.pitch)
-        *reinterpret_cast<uint2*>(it.c.data + static_cast<int64_t>(row0 + r) * it.c.pitch + byte) =
+      if (inside || (row0 + r < it.rows && byte < it.c.pitch))
+        *reinterpret_cast<uint2*>(out + static_cast<int64_t>(k * (kThreads / 8)) * it.c.pitch) =
             make_uint2(e2m1_pack8(v), e2m1_pack8(v + 8));
       // [atom][r % 32][r / 32][block]: the tile's half of each 16 bytes
       const int b = kNv ? c16 : c16 >> 1;
@@ -316,7 +358,8 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const Item one, const I
   {
     constexpr int kCw = kNv ? 2 : 1;
     const int c0 = (t % (kTile / kCw)) * kCw, rb = t / (kTile / kCw);
-    const uint8_t* s = smem + rb * kBlk * kPitch + c0 * sizeof(T);
+    constexpr int kPiece = 16 / sizeof(T);
+    const uint8_t* s = smem + rb * kBlk * kPitch + swizzled<T>(c0 / kPiece) * 16 + c0 % kPiece * sizeof(T);
     uint32_t x[kCw][kBlk];  // as fp32 bits
     uint32_t a[kCw] = {}, both = 0u;
     float m[kCw] = {};
@@ -366,14 +409,15 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const Item one, const I
     }
   }
   __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kTile * 4 / kThreads; ++k) {
-    const int u = t + k * kThreads;
-    const int c = u >> 2, q = u & 3;
+  {
+    const int c = t >> 2, q = t & 3;
     const int64_t byte = static_cast<int64_t>(row0) / 2 + q * 8;
-    if (col0 + c < it.cols && byte < it.r.pitch)
-      *reinterpret_cast<uint2*>(it.r.data + static_cast<int64_t>(col0 + c) * it.r.pitch + byte) =
-          *reinterpret_cast<const uint2*>(stage + c * kStagePitch + q * 8);
+    uint8_t* out = it.r.data + static_cast<int64_t>(col0 + c) * it.r.pitch + byte;
+#pragma unroll
+    for (int k = 0; k < kTile * 4 / kThreads; ++k)
+      if (inside || (col0 + c + k * (kThreads / 4) < it.cols && byte < it.r.pitch))
+        *reinterpret_cast<uint2*>(out + static_cast<int64_t>(k * (kThreads / 4)) * it.r.pitch) =
+            *reinterpret_cast<const uint2*>(stage + (c + k * (kThreads / 4)) * kStagePitch + q * 8);
   }
   if (kNv) {
     if (t < 32 && ty < it.r.atoms)
@@ -390,7 +434,7 @@ struct Launch {
   const Item* one;         // a single matrix, or
   const Item* items;       // a list
   const TileRef* tiles;
-  int ntiles;
+  dim3 grid;
   int dtype, format;
   bool cols, rows, vec;    // vec: every source's rows start on 16-byte boundaries
 };
@@ -398,14 +442,16 @@ struct Launch {
 template <typename T, bool kNv, bool kCols, bool kRows>
 cudaError_t launch_quant_t(const Launch& l, cudaStream_t st) {
   const int smem = (kRows || !l.vec ? kTileR * Src<T>::kPitch : 0) + (kRows ? kTile * kStagePitch : 0);
-  quant_kernel<T, kNv, kCols, kRows><<<l.ntiles, kThreads, smem, st>>>(l.one ? *l.one : Item{}, l.items, l.tiles);
+  if (l.one) quant_kernel<T, kNv, kCols, kRows, false><<<l.grid, kThreads, smem, st>>>(*l.one, nullptr, nullptr);
+  else quant_kernel<T, kNv, kCols, kRows, true><<<l.grid, kThreads, smem, st>>>(Item{}, l.items, l.tiles);
   return cudaGetLastError();
 }
 
 template <typename T, bool kNv>
 cudaError_t launch_quant_n(const Launch& l, cudaStream_t st) {
   if (kNv) {
-    amax_kernel<T><<<l.ntiles, kThreads, 0, st>>>(l.one ? *l.one : Item{}, l.items, l.tiles);
+    if (l.one) amax_kernel<T, false><<<l.grid, kThreads, 0, st>>>(*l.one, nullptr, nullptr);
+    else amax_kernel<T, true><<<l.grid, kThreads, 0, st>>>(Item{}, l.items, l.tiles);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -475,12 +521,16 @@ __device__ __forceinline__ void store_values(T* out, const float* v, int len) {
 }
 
 // Rows of the destination on 16-byte boundaries: a unit is 16 values, within one block.
-template <typename T, bool kNv>
-__global__ void __launch_bounds__(kThreads) dequant_kernel(const Deq one, const Deq* __restrict__ items,
+template <typename T, bool kNv, bool kList>
+__global__ void __launch_bounds__(kThreads) dequant_kernel(const __grid_constant__ Deq one, const Deq* __restrict__ items,
                                                            const DeqRef* __restrict__ refs) {
   DeqRef ref{0, 0, static_cast<int64_t>(blockIdx.x) * kDeqChunk};
-  if (refs != nullptr) ref = refs[blockIdx.x];
-  const Deq it = items != nullptr ? items[ref.item] : one;
+  Deq listed;
+  if constexpr (kList) {
+    ref = refs[blockIdx.x];
+    listed = items[ref.item];
+  }
+  const Deq& it = kList ? listed : one;
   const int64_t left = static_cast<int64_t>(it.rows) * it.units - ref.first;
   const int n = static_cast<int>(left < kDeqChunk ? left : kDeqChunk);
   const float g = kNv ? it.ts[0] : 1.0f;
@@ -510,12 +560,16 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const Deq one, const 
 // up to a 16-byte boundary, the units after it are eight values each, stored
 // as whole 16-byte pieces (codes are four bits, so any eight of them are a
 // funnel shift of two words).
-template <typename T, bool kNv>
-__global__ void __launch_bounds__(kThreads) dequant_any_kernel(const Deq one, const Deq* __restrict__ items,
+template <typename T, bool kNv, bool kList>
+__global__ void __launch_bounds__(kThreads) dequant_any_kernel(const __grid_constant__ Deq one, const Deq* __restrict__ items,
                                                            const DeqRef* __restrict__ refs) {
   DeqRef ref{0, 0, static_cast<int64_t>(blockIdx.x) * kDeqChunk};
-  if (refs != nullptr) ref = refs[blockIdx.x];
-  const Deq it = items != nullptr ? items[ref.item] : one;
+  Deq listed;
+  if constexpr (kList) {
+    ref = refs[blockIdx.x];
+    listed = items[ref.item];
+  }
+  const Deq& it = kList ? listed : one;
   const int64_t left = static_cast<int64_t>(it.rows) * it.units - ref.first;
   const int n = static_cast<int>(left < kDeqChunk ? left : kDeqChunk);
   const float g = kNv ? it.ts[0] : 1.0f;
@@ -559,8 +613,13 @@ template <typename T, bool kNv>
 cudaError_t launch_dequant_t(const Deq& one, const Deq* items, const DeqRef* refs, int64_t nblocks, bool vec,
                              cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(nblocks));
-  if (vec) dequant_kernel<T, kNv><<<grid, kThreads, 0, st>>>(one, items, refs);
-  else dequant_any_kernel<T, kNv><<<grid, kThreads, 0, st>>>(one, items, refs);
+  if (items != nullptr) {
+    if (vec) dequant_kernel<T, kNv, true><<<grid, kThreads, 0, st>>>(one, items, refs);
+    else dequant_any_kernel<T, kNv, true><<<grid, kThreads, 0, st>>>(one, items, refs);
+  } else {
+    if (vec) dequant_kernel<T, kNv, false><<<grid, kThreads, 0, st>>>(one, items, refs);
+    else dequant_any_kernel<T, kNv, false><<<grid, kThreads, 0, st>>>(one, items, refs);
+  }
   return cudaGetLastError();
 }
 
@@ -608,6 +667,7 @@ muon_status_t make_item(const muon_fp4_source_t& s, Item& it, bool& empty) {
   it.rows = static_cast<int32_t>(s.rows);
   it.cols = static_cast<int32_t>(s.cols);
   it.tiles_x = static_cast<int32_t>(tx);
+  it.tiles_y = static_cast<int32_t>(ty);
   it.vec = (a % 16 == 0 && s.ld * es % 16 == 0) ? 1 : 0;
   auto form = [](const muon_fp4_matrix_t& m) {
     return Form{static_cast<uint8_t*>(m.data), static_cast<uint8_t*>(m.scales), m.tensor_scale, pitch_of(m.k),
@@ -619,9 +679,7 @@ muon_status_t make_item(const muon_fp4_source_t& s, Item& it, bool& empty) {
   return MUON_OK;
 }
 
-int tiles_of(const Item& it) {
-  return it.tiles_x * ((it.rows + kAtomRows - 1) / kAtomRows * (kAtomRows / kTileR));
-}
+int tiles_of(const Item& it) { return it.tiles_x * it.tiles_y; }
 
 template <class List>
 void item_ranges(const muon_fp4_source_t& s, List& reads, List& writes) {
@@ -656,8 +714,7 @@ struct muon_fp4_plan_s {
   int device = 0;
   int dtype = 0, format = 0, values_dtype = -1;
   bool cols = false, rows = false, vec = true;
-  int nitems = 0, ngroups = 0;
-  int* groups = nullptr;  // host: first tile of each group, then the number of tiles
+  int nitems = 0, ntiles = 0;
   int64_t ndeq = 0, ndeq_vec = 0;
   uint8_t* dmem = nullptr;
   Item* items_d = nullptr;
@@ -699,7 +756,9 @@ muon_status_t muon_fp4_quantize(const muon_fp4_source_t* src, void* stream) {
       return MUON_ERR_CUDA;
     }
   }
-  const Launch l{&it, nullptr, nullptr, tiles_of(it), src->src_dtype, format, c, r, it.vec != 0};
+  const unsigned gy = it.tiles_y < kGridY ? it.tiles_y : kGridY;
+  const Launch l{&it, nullptr, nullptr, dim3(it.tiles_x, gy, (it.tiles_y + kGridY - 1) / kGridY), src->src_dtype, format,
+                 c, r, it.vec != 0};
   return launch_quant(l, st) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
@@ -735,8 +794,6 @@ muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs,
     std::vector<DeqRef> refs;      // vector kernel first, then the others
     std::vector<DeqRef> refs_any;
     std::vector<ByteRange> reads, writes;
-    std::vector<int> groups;
-    int64_t group_bytes = kGroupBytes;
     bool vec = true;
     const bool c = srcs[0].along_cols.format >= 0, r = srcs[0].along_rows.format >= 0;
     const int32_t format = c ? srcs[0].along_cols.format : srcs[0].along_rows.format;
@@ -757,14 +814,7 @@ muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs,
       const int nt = tiles_of(it);
       if (static_cast<int64_t>(tiles.size()) + nt > 0x7fffffff) return MUON_ERR_UNSUPPORTED;
       vec = vec && it.vec;
-      // MX needs no second pass: one group
-      const int64_t bytes = s.rows * s.cols * size_of(s.src_dtype);
-      if (tiles.empty() || (format == MUON_FP4_NV && group_bytes + bytes > kGroupBytes)) {
-        groups.push_back(static_cast<int>(tiles.size()));
-        group_bytes = 0;
-      }
-      group_bytes += bytes;
-      for (int k = 0; k < nt; ++k) tiles.push_back(TileRef{id, k});
+      for (int k = 0; k < nt; ++k) tiles.push_back(TileRef{id, k % it.tiles_x, k / it.tiles_x});
       if (values_dtype >= 0)
         for (int f = 0; f < 2; ++f) {
           if (f == 0 ? !c : !r) continue;
@@ -797,14 +847,7 @@ muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs,
     pl->rows = r;
     pl->nitems = static_cast<int>(items.size());
     pl->vec = vec;
-    pl->ngroups = static_cast<int>(groups.size());
-    groups.push_back(static_cast<int>(tiles.size()));
-    pl->groups = new (std::nothrow) int[groups.size()];
-    if (pl->groups == nullptr) {
-      delete pl;
-      return MUON_ERR_NO_MEMORY;
-    }
-    std::copy(groups.begin(), groups.end(), pl->groups);
+    pl->ntiles = static_cast<int>(tiles.size());
     pl->ndeq = static_cast<int64_t>(refs.size());
     pl->ndeq_vec = ndeq_vec;
     pl->last_stream = static_cast<cudaStream_t>(stream);
@@ -815,7 +858,6 @@ muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs,
                    br = up(refs.size() * sizeof(DeqRef));
       if (cudaMalloc(&pl->dmem, bi + bt + ba + bd + br) != cudaSuccess) {
         cudaGetLastError();
-        delete[] pl->groups;
         delete pl;
         return MUON_ERR_NO_MEMORY;
       }
@@ -834,7 +876,6 @@ muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs,
           !put(pl->refs_d, refs.data(), refs.size() * sizeof(DeqRef))) {
         cudaGetLastError();
         cudaFree(pl->dmem);
-        delete[] pl->groups;
         delete pl;
         return MUON_ERR_CUDA;
       }
@@ -857,13 +898,8 @@ muon_status_t muon_fp4_run(muon_fp4_plan_t pl, void* stream) {
     cudaGetLastError();
     return MUON_ERR_CUDA;
   }
-  for (int k = 0; k < pl->ngroups; ++k) {
-    const int first = pl->groups[k], last = pl->groups[k + 1];
-    const Launch l{nullptr, pl->items_d, pl->tiles_d + first, last - first, pl->dtype, pl->format, pl->cols, pl->rows,
-                   pl->vec};
-    if (launch_quant(l, st) != cudaSuccess) return MUON_ERR_CUDA;
-  }
-  return MUON_OK;
+  const Launch l{nullptr, pl->items_d, pl->tiles_d, dim3(pl->ntiles), pl->dtype, pl->format, pl->cols, pl->rows, pl->vec};
+  return launch_quant(l, st) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
 muon_status_t muon_fp4_values(muon_fp4_plan_t pl, void* stream) {
@@ -886,7 +922,6 @@ void muon_fp4_destroy(muon_fp4_plan_t pl) {
   cudaStreamSynchronize(pl->last_stream);
   cudaGetLastError();
   cudaFree(pl->dmem);
-  delete[] pl->groups;
   delete pl;
 }
 
