@@ -469,7 +469,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll 8
               for (int r = 0; r < nr; ++r) {
                 const float f = __uint_as_float(w[r * 32 + (lane ^ r)]);
-                out[r * g.ldo + lane] = g.accumulate ? out[r * g.ldo + lane] + f : f;
+                // added where it lies (one addition an element), so that no load is waited for
+                if (g.accumulate) atomicAdd(out + r * g.ldo + lane, f);
+                else out[r * g.ldo + lane] = f;
               }
             }
             __syncwarp();

@@ -264,12 +264,13 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const __grid_constant__
   uint8_t* stage = smem + kTileR * kPitch;         // [128][kStagePitch] codes along the rows
   __shared__ __align__(16) uint8_t sc_c[kAtomsC * 256];
   __shared__ __align__(16) uint8_t sc_r[kAtomBytes];
-  const TileRef ref = my_tile<kList>(tiles);
+  // NV: the tiles that the pass before read last come first, being in L2
+  const TileRef ref = kList && kNv ? tiles[gridDim.x - 1 - blockIdx.x] : my_tile<kList>(tiles);
   Item listed;
   if constexpr (kList) listed = items[ref.item];  // all of it at once
   const Item& it = kList ? listed : one;
-  const int ty = ref.ty, tx = ref.tx;
-  if (!kList && ty >= it.tiles_y) return;
+  if (!kList && ref.ty >= it.tiles_y) return;
+  const int tx = ref.tx, ty = !kList && kNv ? it.tiles_y - 1 - ref.ty : ref.ty;
   const int row0 = ty * kTileR, col0 = tx * kTile;
   const bool inside = row0 + kTileR <= it.rows && col0 + kTile <= it.cols;
   const int half = ty & 1;  // of the 128 rows of an atom
