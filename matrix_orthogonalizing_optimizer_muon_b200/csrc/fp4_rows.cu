@@ -10,7 +10,8 @@
 //
 //   W  goes to shared memory by cp.async, in steps of 128 k of a warp's 16
 //      rows, kDepth - 1 steps ahead (plain loads into registers were moved
-//      down to their use by the compiler: 36 us instead of XX for 65536 x 2048).  A code becomes an fp16 by one conversion for two.
+//      down to their use by the compiler: 36 us instead of 25 for
+//      65536 x 2048).  A code becomes an fp16 by one conversion for two.
 //      NV: times the block's scale, exactly (e2m1 x e4m3 has at most six
 //      significant bits within fp16's range).  MX: the exponent of a scale may
 //      be outside fp16's range, so the products of a block are summed from
@@ -31,13 +32,12 @@ namespace {
 using namespace muon;
 using namespace muon::fp4;
 
-constexpr int kWarpsR = 8;
-constexpr int kThreadsR = 32 * kWarpsR;
 constexpr int kStepK = 128;          // k of a step: 32 codes a thread
 constexpr int kDepth = 4;            // ring of steps of a warp
 constexpr int kStepBytes = 1024 + 128;  // codes of 16 rows, then 8 bytes of scales a row
 constexpr int kMaxK = 10240;         // k of X in shared memory at a time
 constexpr int kXBudget = 164 * 1024; // bytes of it
+constexpr int kSmemMax = 226 * 1024;
 constexpr int kMxShift = 16;         // MX scales are taken times 2^-16, so that a sum of scaled products
                                      // overflows only where a block scale is above 2^121
 
@@ -88,15 +88,15 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-template <bool kNv, int kNg>
-__global__ void __launch_bounds__(kThreadsR, 2) fp4_rows_kernel(const RowsArgs g) {
+template <bool kNv, int kNg, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(const RowsArgs g) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t amax[8 * kNg];  // bits of the largest finite magnitude of each row of X
   uint8_t* rings = smem + 8 * kNg * g.xpitch;
-  float* part = reinterpret_cast<float*>(rings + kWarpsR * kDepth * kStepBytes);  // [warp][16 * 8 * kNg], k split only
+  float* part = reinterpret_cast<float*>(rings + kWarps * kDepth * kStepBytes);  // [warp][16 * 8 * kNg], k split only
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gr = lane >> 2, t4 = lane & 3;
-  const int ks = warp % g.ks, rw = warp / g.ks, per = kWarpsR / g.ks;
+  const int ks = warp % g.ks, rw = warp / g.ks, per = kWarps / g.ks;
   const int t0 = blockIdx.y * g.tg;
   const int nt = min(g.tg, g.t - t0);
   const int ngroups = (g.n + 16 * per - 1) / (16 * per);
@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(kThreadsR, 2) fp4_rows_kernel(const RowsArgs g
   auto stage = [&](int k0) {
     const int kn = min(g.kc, g.k - k0);
     const int pieces = (kn + kStepK - 1) / kStepK * (kStepK / 8);
-    const int wpr = nt > 4 ? 1 : nt > 2 ? 2 : nt > 1 ? 4 : 8;  // warps per row
-    const int first = warp / wpr, rstep = kWarpsR / wpr, p0 = (warp - first * wpr) * 32 + lane, pstep = wpr * 32;
+    const int wpr = nt > kWarps / 2 ? 1 : kWarps / (nt > 4 ? 8 : nt > 2 ? 4 : nt);  // warps per row
+    const int first = warp / wpr, rstep = kWarps / wpr, p0 = (warp - first * wpr) * 32 + lane, pstep = wpr * 32;
     auto piece = [&](const unsigned short* src, bool vec, int p) {
       uint4 q = make_uint4(0u, 0u, 0u, 0u);
       if (vec && p * 8 + 8 <= kn) {
@@ -378,15 +378,34 @@ __global__ void __launch_bounds__(kThreadsR, 2) fp4_rows_kernel(const RowsArgs g
   }
 }
 
-template <bool kNv, int kNg>
-cudaError_t launch_rows(const RowsArgs& g, dim3 grid, int smem, cudaStream_t st) {
+template <bool kNv, int kNg, int kWarps>
+cudaError_t launch_rows_w(const RowsArgs& g, int ctas, int smem, cudaStream_t st) {
+  const int per = kWarps / g.ks;
+  const int groups = ((g.n + 15) / 16 + per - 1) / per;
+  const dim3 grid(groups < ctas ? groups : ctas, (g.t + g.tg - 1) / g.tg);
+  auto kernel = fp4_rows_kernel<kNv, kNg, kWarps>;
   if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(fp4_rows_kernel<kNv, kNg>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  fp4_rows_kernel<kNv, kNg><<<grid, kThreadsR, smem, st>>>(g);
+  kernel<<<grid, 32 * kWarps, smem, st>>>(g);
   return cudaGetLastError();
+}
+
+// 16 warps of 128 registers a SM: up to eight rows of X as two CTAs, whose
+// copies of X are small and whose barriers overlap (65536 x 2048, NV, t = 1:
+// 19.6 us against 20.3 us as one CTA; 2048 x 8192 7.2 against 8.6 us), more
+// rows as one CTA, which copies X once (t = 16: 26.6 against 27.7 us, t = 32:
+// 39.8 against 46.1 us); eight warps where X takes the shared memory.  (24
+// warps of 80 registers spill: t = 16 39.9 us.)
+template <bool kNv, int kNg>
+cudaError_t launch_rows(const RowsArgs& g, int sms, cudaStream_t st) {
+  auto smem = [&](int warps) {
+    return 8 * kNg * g.xpitch + warps * (kDepth * kStepBytes + (g.ks > 1 ? 128 * kNg * 4 : 0));
+  };
+  const bool two = 2 * (smem(8) + 2048) <= kSmemMax;
+  if ((kNg == 1 && two) || smem(16) > kSmemMax) return launch_rows_w<kNv, kNg, 8>(g, two ? 2 * sms : sms, smem(8), st);
+  return launch_rows_w<kNv, kNg, 16>(g, sms, smem(16), st);
 }
 
 }  // namespace
@@ -430,19 +449,15 @@ extern "C" muon_status_t muon_fp4_rows_product(const void* x, int64_t t, int64_t
   int ng = t <= 8 ? 1 : t <= 16 ? 2 : 4;
   while (ng > 1 && 8 * ng * g.xpitch > kXBudget) ng /= 2;
   g.tg = 8 * ng;
+  // k split: until the row tiles give every warp of the GPU one, or a warp has only two steps left
   const int64_t tiles = (w->rows + 15) / 16;
+  const int steps = (g.kc + kStepK - 1) / kStepK;
   g.ks = 1;
-  while (g.ks < kWarpsR && tiles * g.ks < 2 * kWarpsR * static_cast<int64_t>(sms)) g.ks *= 2;
-  const int per = kWarpsR / g.ks;
-  const int64_t groups = (tiles + per - 1) / per;
-  const int smem = 8 * ng * g.xpitch + kWarpsR * kDepth * kStepBytes + (g.ks > 1 ? kWarpsR * 128 * ng * 4 : 0);
-  const int resident = smem <= 100 * 1024 ? 2 : 1;
-  const int64_t want = static_cast<int64_t>(sms) * resident;
-  const dim3 grid(static_cast<unsigned>(groups < want ? groups : want), static_cast<unsigned>((t + g.tg - 1) / g.tg));
+  while (g.ks < 8 && tiles * g.ks < 16 * static_cast<int64_t>(sms) && steps > 2 * g.ks) g.ks *= 2;
   const bool nv = w->format == MUON_FP4_NV;
   cudaError_t e;
-  if (ng == 1) e = nv ? launch_rows<true, 1>(g, grid, smem, st) : launch_rows<false, 1>(g, grid, smem, st);
-  else if (ng == 2) e = nv ? launch_rows<true, 2>(g, grid, smem, st) : launch_rows<false, 2>(g, grid, smem, st);
-  else e = nv ? launch_rows<true, 4>(g, grid, smem, st) : launch_rows<false, 4>(g, grid, smem, st);
+  if (ng == 1) e = nv ? launch_rows<true, 1>(g, sms, st) : launch_rows<false, 1>(g, sms, st);
+  else if (ng == 2) e = nv ? launch_rows<true, 2>(g, sms, st) : launch_rows<false, 2>(g, sms, st);
+  else e = nv ? launch_rows<true, 4>(g, sms, st) : launch_rows<false, 4>(g, sms, st);
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
