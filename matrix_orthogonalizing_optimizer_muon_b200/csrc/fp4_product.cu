@@ -355,7 +355,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const int quad = warp & 3, half = (warp - kEpi0) >> 2;
     constexpr int kPer = kBn / 2 / 32;  // 32-column blocks of a warp
     const uint32_t tempty = kCg == 2 ? map_to_rank(tempty_bar, 0) : tempty_bar;
-    const float ga = kNv ? *g.ga : 1.0f, gb = kNv ? *g.gb : 1.0f;
+    // the smaller scale first: nothing passes fp32's range that the result does not pass
+    const float sa = kNv ? *g.ga : 1.0f, sb = kNv ? *g.gb : 1.0f;
+    const float ga = fabsf(sa) < fabsf(sb) ? sa : sb, gb = fabsf(sa) < fabsf(sb) ? sb : sa;
     const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * (kBn / 2);
     uint8_t* stg = smem + C::kEpi + (warp - kEpi0) * kStagingBytes;
     uint32_t tphase = 0;

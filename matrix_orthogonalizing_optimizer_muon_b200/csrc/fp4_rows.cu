@@ -92,7 +92,7 @@ template <bool kNv, int kNg, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(const RowsArgs g) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t amax[8 * kNg];  // bits of the largest finite magnitude of each row of X
-  uint8_t* rings = smem + 8 * kNg * g.xpitch;
+  uint8_t* rings = smem + min(g.tg, g.t) * g.xpitch;
   float* part = reinterpret_cast<float*>(rings + kWarps * kDepth * kStepBytes);  // [warp][16 * 8 * kNg], k split only
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gr = lane >> 2, t4 = lane & 3;
@@ -144,9 +144,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
   // of 128 the 16-byte pieces lie in the order in which the four threads of a
   // row take them: NV thread t4's i-th piece (8 values of its 32) at 4 i + t4,
   // MX in order.
-  // Few rows are each spread over several warps.  Shared memory of rows that
-  // X does not have is left as it is: it reaches only their own columns of the
-  // products, which are not written.
+  // Few rows are each spread over several warps.
   auto stage = [&](int k0) {
     const int kn = min(g.kc, g.k - k0);
     const int pieces = (kn + kStepK - 1) / kStepK * (kStepK / 8);
@@ -218,8 +216,11 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
   };
 
   const int npass = (g.k + g.kc - 1) / g.kc;
-  const uint8_t* xs = smem + gr * g.xpitch + t4 * 16;
-  const float ts = kNv ? *g.ts : 1.0f;
+  // columns of the products that X has no row for read its last one; they are not written
+  int xrow[kNg];
+#pragma unroll
+  for (int q = 0; q < kNg; ++q) xrow[q] = min(8 * q + gr, nt - 1) * g.xpitch + t4 * 16;
+  const float unit = kNv ? *g.ts : static_cast<float>(1 << kMxShift);
   bool staged = false;
   for (int grp = blockIdx.x; grp < ngroups; grp += gridDim.x) {
     float total[kNg][4];
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
       for (int q = 0; q < kNg; ++q)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[q][i] = 0.0f;
-      const uint8_t* xj = xs + ks * (kStepK * 2);
+      const uint8_t* xj = smem + ks * (kStepK * 2);
       auto step = [&](int i, int d) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");  // step i has landed
         __syncwarp();  // for every lane, and step i - 1 has been read by every lane
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
           }
 #pragma unroll
           for (int q = 0; q < kNg; ++q) {
-            const uint4 x = *reinterpret_cast<const uint4*>(xj + q * 8 * g.xpitch + b * 64);
+            const uint4 x = *reinterpret_cast<const uint4*>(xj + xrow[q] + b * 64);
             if (kNv) {
               mma16816(acc[q], lo[0], hi[0], lo[1], hi[1], x.x, x.y);
               mma16816(acc[q], lo[2], hi[2], lo[3], hi[3], x.z, x.w);
@@ -336,12 +337,17 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
       for (int d = 0; d < kDepth - 1; ++d)
         if (i + d < ni) step(i + d, d);
       __syncwarp();  // the ring is read before the next pass or tile fills it
+      // undo X's powers of two; the factor that shrinks comes first, so that
+      // nothing passes fp32's range that the result does not pass
 #pragma unroll
       for (int q = 0; q < kNg; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          total[q][i] += acc[q][i] * pow2(exponent_of(amax[8 * q + 2 * t4 + (i & 1)])) *
-                         (kNv ? 1.0f : static_cast<float>(1 << kMxShift));
+        for (int j = 0; j < 2; ++j) {
+          const int e = exponent_of(amax[min(8 * q + 2 * t4 + j, nt - 1)]);
+          const float f0 = e < 0 ? pow2(e) : unit, f1 = e < 0 ? unit : pow2(e);
+          total[q][j] += acc[q][j] * f0 * f1;
+          total[q][j + 2] += acc[q][j + 2] * f0 * f1;
+        }
     }
     if (g.ks > 1) {
       // the first warp of a row tile adds the others' sums, in order
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
         const int row = (grp * per + rw) * 16 + gr + (i >> 1) * 8;
         const int t = 8 * q + 2 * t4 + (i & 1);
         if (row >= g.n || t >= nt) continue;
-        const float v = kNv ? total[q][i] * ts : total[q][i];
+        const float v = total[q][i];
         const int64_t at = static_cast<int64_t>(t0 + t) * g.ldo + row;
         if (g.out_dtype == MUON_DT_BF16) static_cast<__nv_bfloat16*>(g.out)[at] = __float2bfloat16_rn(v);
         else static_cast<float*>(g.out)[at] = v;
@@ -401,10 +407,13 @@ cudaError_t launch_rows_w(const RowsArgs& g, int ctas, int smem, cudaStream_t st
 template <bool kNv, int kNg>
 cudaError_t launch_rows(const RowsArgs& g, int sms, cudaStream_t st) {
   auto smem = [&](int warps) {
-    return 8 * kNg * g.xpitch + warps * (kDepth * kStepBytes + (g.ks > 1 ? 128 * kNg * 4 : 0));
+    return (g.t < g.tg ? g.t : g.tg) * g.xpitch + warps * (kDepth * kStepBytes + (g.ks > 1 ? 128 * kNg * 4 : 0));
   };
   const bool two = 2 * (smem(8) + 2048) <= kSmemMax;
-  if ((kNg == 1 && two) || smem(16) > kSmemMax) return launch_rows_w<kNv, kNg, 8>(g, two ? 2 * sms : sms, smem(8), st);
+  // fewer row tiles than 16 warps a SM take: CTAs of eight reach more SMs
+  // (many rows of X are better copied by 16 warps)
+  const bool few = static_cast<int64_t>((g.n + 15) / 16) * g.ks < 16 * static_cast<int64_t>(sms);
+  if ((kNg == 1 && (two || few)) || smem(16) > kSmemMax) return launch_rows_w<kNv, kNg, 8>(g, two ? 2 * sms : sms, smem(8), st);
   return launch_rows_w<kNv, kNg, 16>(g, sms, smem(16), st);
 }
 

@@ -265,6 +265,20 @@ def test_product_with_an_arbitrary_tensor_scale(fp4, m):
     check_rows(fp4.fp4_rows_product(x, b, out_dtype=torch.float32), x64, b64 * fb, torch.float32)
 
 
+@pytest.mark.parametrize("m", [40, 2500])
+@pytest.mark.parametrize("ea,eb", [(110, -95), (-95, 110), (-60, -50), (60, 50)])
+def test_product_of_operands_far_apart(fp4, m, ea, eb):
+    """Tensor scales at the ends of fp32's range whose product is within it."""
+    a64, x = values((m, 96), 43, "fp32", 0.0)
+    b64, w = values((1400, 96), 44, "fp32", 0.0)
+    x.mul_(2.0 ** ea)
+    w.mul_(2.0 ** eb)
+    for fmt in ("mx", "nv"):
+        qv = lambda t: o.quantize(t.double().cpu().numpy(), fmt).values()  # noqa: E731
+        got = fp4.fp4_product(fp4.fp4_quantize(x, fmt=fmt), fp4.fp4_quantize(w, fmt=fmt), out_dtype=torch.float32)
+        check_product(got, qv(x), qv(w), torch.float32)
+
+
 def test_products_of_nothing(fp4):
     """No rows, no columns, no k."""
     for fmt in ("mx", "nv"):
@@ -307,6 +321,74 @@ def test_rows_product_matches_the_oracle(fp4, t, n, k, fmt):
     w, w64 = quantized(fp4, (n, k), 24, fmt)
     for dt in DT.values():
         check_rows(fp4.fp4_rows_product(x, w, out_dtype=dt), x64, w64, dt)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("t,n,k", [(1, 40, 10240), (3, 50, 10241), (20, 33, 20600), (32, 200, 10239)])
+def test_rows_product_long_k(fp4, t, n, k, fmt):
+    """k at, next to and past what shared memory holds of X at a time; a row
+    alone gives the bits that it gives among others."""
+    x64, x = values((t, k), 40, "bf16", 1.0)
+    w, w64 = quantized(fp4, (n, k), 41, fmt)
+    got = fp4.fp4_rows_product(x, w, out_dtype=torch.float32)
+    check_rows(got, x64, w64, torch.float32)
+    assert torch.equal(fp4.fp4_rows_product(x[t - 1:], w, out_dtype=torch.float32), got[t - 1:])
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_rows_product_extreme_rows(fp4, fmt):
+    """Rows of zeros, of subnormals, near bf16's largest values, and of values
+    2^40 apart: each keeps its own precision."""
+    k, n = 256, 48
+    x = torch.randn(6, k, device="cuda").bfloat16()
+    x[1] = 0
+    x[2] = (torch.randn(k, device="cuda") * 2.0 ** -128).bfloat16()
+    x[3] = (torch.randn(k, device="cuda").clamp(-1, 1) * 2.0 ** 118).bfloat16()
+    x[4, ::2] *= 2.0 ** 20
+    x[4, 1::2] *= 2.0 ** -20
+    x[5] = 2.0 ** -133
+    w, w64 = quantized(fp4, (n, k), 42, fmt, 0.0)
+    got = fp4.fp4_rows_product(x, w, out_dtype=torch.float32)
+    check_rows(got, x.double().cpu().numpy(), w64, torch.float32)
+    assert (got[1] == 0).all()
+
+
+def test_offsets_past_32_bits(fp4):
+    """Codes, sources and outputs of more than 2^31 bytes and 2^31 elements:
+    the last rows are those of the last rows alone."""
+    x = torch.empty(70000, 65536, dtype=torch.bfloat16, device="cuda")
+    for i in range(0, 70000, 5000):
+        x[i:i + 5000] = torch.randn(5000, 65536, device="cuda")
+    m = fp4.fp4_quantize(x, fmt="mx")
+    tail = fp4.fp4_quantize(x[-130:], fmt="mx")
+    assert m.data.numel() > 2 ** 31
+    assert torch.equal(m.data.view(70000, -1)[-130:], tail.data.view(130, -1))
+    v = torch.empty_like(x)
+    m.dequantize(out=v)
+    assert torch.equal(v[-130:], tail.dequantize())
+    del v
+    tok = x[:2, :].contiguous()
+    assert torch.equal(fp4.fp4_rows_product(tok, m)[:, -130:], fp4.fp4_rows_product(tok, tail))
+    del x, m
+    a = fp4.fp4_quantize(torch.randn(70000, 64, device="cuda"), fmt="mx")
+    b = fp4.fp4_quantize(torch.randn(32768, 64, device="cuda"), fmt="mx")
+    out = fp4.fp4_product(a, b)
+    assert out.numel() > 2 ** 31
+    last = fp4.fp4_quantize(a.dequantize()[-112:], fmt="mx")
+    assert torch.equal(out[-112:], fp4.fp4_product(last, b))
+    assert fp4.fp4_status() == 0
+
+
+@pytest.mark.parametrize("along", ["cols", "rows"])
+def test_more_tile_rows_than_a_grid_dimension(fp4, along):
+    """Rows past 32768 tiles of 64."""
+    rows = 32768 * 64 + 100
+    x = torch.randn(rows, 33, device="cuda").bfloat16()
+    m = fp4.fp4_quantize(x, fmt="mx", along=along)
+    v = m.dequantize()
+    cut = 32768 * 64 - 64
+    tail = fp4.fp4_quantize(x[cut:], fmt="mx", along=along).dequantize()
+    assert torch.equal(v[cut:] if along == "cols" else v[:, cut:], tail)
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
