@@ -32,6 +32,10 @@ using namespace muon::fp4;
 
 constexpr int kTileR = 64, kTile = 128;  // rows and columns of a tile
 constexpr int kThreads = 256;
+// NV matrices of up to so many values (a few tokens) are looked through by
+// every CTA instead of in a pass before: one launch instead of a memset and
+// two.  A CTA reads 64 values a thread at most.
+constexpr int64_t kSmall = 16384;
 
 constexpr int kStagePitch = kTileR / 2 + 8;  // a staged row of codes along the rows
 static_assert(kTileR * kTile * 4 + kTile * kStagePitch <= 48 * 1024, "dynamic shared memory without opt-in");
@@ -50,7 +54,7 @@ struct Item {
   int32_t rows, cols;
   int32_t tiles_x, tiles_y;  // tiles of 128 columns and 64 rows, the latter an even number
   int32_t vec;     // rows start on 16-byte boundaries
-  unsigned* amax;  // NV: bits of the largest finite magnitude
+  unsigned* amax;  // NV: bits of the largest finite magnitude; NULL (a single small matrix): found by every CTA
   Form c, r;       // along the columns [rows, cols], along the rows [cols, rows]
 };
 
@@ -251,6 +255,27 @@ __global__ void __launch_bounds__(kThreads) amax_kernel(const __grid_constant__ 
   }
 }
 
+// The same of a whole small matrix by every CTA for itself.
+template <typename T>
+__device__ uint32_t small_amax(const Item& it) {
+  using Raw = typename Src<T>::Raw;
+  __shared__ uint32_t part[kThreads / 32];
+  const uint32_t n = static_cast<uint32_t>(it.rows) * static_cast<uint32_t>(it.cols);
+  uint32_t a = 0u;
+#pragma unroll 8
+  for (uint32_t e = threadIdx.x; e < n; e += kThreads) {
+    const uint32_t r = e / static_cast<uint32_t>(it.cols);
+    const Raw* p = static_cast<const Raw*>(it.src) + static_cast<int64_t>(r) * it.ld + (e - r * it.cols);
+    a = max(a, finite_bits(static_cast<uint32_t>(__ldg(p)) << (sizeof(T) == 4 ? 0 : 16)));
+  }
+  a = __reduce_max_sync(0xffffffffu, a);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) a = max(a, part[i]);
+  return a;
+}
+
 // ---------------------------------------------------------------- quantisation
 template <typename T, bool kNv, bool kCols, bool kRows, bool kList>
 __global__ void __launch_bounds__(kThreads) quant_kernel(const __grid_constant__ Item one,
@@ -277,7 +302,7 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const __grid_constant__
   const int t = threadIdx.x;
   MatrixScale g = {};
   if (kNv) {
-    const uint32_t bits = *it.amax;
+    const uint32_t bits = !kList && it.amax == nullptr ? small_amax<T>(it) : *it.amax;
     g = matrix_scale(bits);
     if ((tx | ty | t) == 0) {
       if (kCols) {
@@ -450,7 +475,7 @@ cudaError_t launch_quant_t(const Launch& l, cudaStream_t st) {
 
 template <typename T, bool kNv>
 cudaError_t launch_quant_n(const Launch& l, cudaStream_t st) {
-  if (kNv) {
+  if (kNv && !(l.one && l.one->amax == nullptr)) {
     if (l.one) amax_kernel<T, false><<<l.grid, kThreads, 0, st>>>(*l.one, nullptr, nullptr);
     else amax_kernel<T, true><<<l.grid, kThreads, 0, st>>>(Item{}, l.items, l.tiles);
     const cudaError_t e = cudaGetLastError();
@@ -750,7 +775,7 @@ muon_status_t muon_fp4_quantize(const muon_fp4_source_t* src, void* stream) {
   const bool c = it.c.data != nullptr, r = it.r.data != nullptr;
   const int format = c ? src->along_cols.format : src->along_rows.format;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (format == MUON_FP4_NV) {
+  if (format == MUON_FP4_NV && src->rows * src->cols > kSmall) {
     it.amax = reinterpret_cast<unsigned*>((c ? it.c.ts : it.r.ts) + 1);
     if (cudaMemsetAsync(it.amax, 0, sizeof(unsigned), st) != cudaSuccess) {
       cudaGetLastError();

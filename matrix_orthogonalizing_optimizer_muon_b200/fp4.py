@@ -123,22 +123,34 @@ class Fp4Matrix:
     def empty(cls, rows: int, k: int, fmt: str = "nv", device=None) -> "Fp4Matrix":
         """Uninitialised storage in one allocation."""
         _check_fmt(fmt)
-        if rows < 0 or k < 0 or rows > _MAX_DIM or k > _MAX_DIM:
-            raise ValueError(f"a 4-bit matrix has 0 to 2^30 rows and columns, not {rows} x {k}")
-        nd, ns = _sizes(fmt, rows, k)
-        off = -(-nd // 256) * 256
-        buf = torch.empty(off + ns + 8, dtype=torch.uint8, device=device if device is not None else "cuda")
-        m = cls.__new__(cls)
-        at = buf.data_ptr()
-        m._set(rows, k, fmt, buf.device, at, at + off, at + off + ns if fmt == "nv" else None)
-        m._parts, m._buf = None, (buf, nd, off, ns)
-        return m
+        return cls._alloc([(rows, k)], fmt, device if device is not None else "cuda")[0]
+
+    @classmethod
+    def _alloc(cls, shapes, fmt, device):
+        """Uninitialised matrices of these shapes in one allocation."""
+        plan, end = [], 0
+        for rows, k in shapes:
+            if rows < 0 or k < 0 or rows > _MAX_DIM or k > _MAX_DIM:
+                raise ValueError(f"a 4-bit matrix has 0 to 2^30 rows and columns, not {rows} x {k}")
+            nd, ns = _sizes(fmt, rows, k)
+            off = end + -(-nd // 256) * 256
+            plan.append((rows, k, end, nd, off, ns))
+            end = off + ns + 256  # the tensor scale, and the next matrix on a 256-byte boundary
+        buf = torch.empty(end, dtype=torch.uint8, device=device)
+        at, dev, nv, out = buf.data_ptr(), buf.device, fmt == "nv", []
+        for rows, k, start, nd, off, ns in plan:
+            m = cls.__new__(cls)
+            m._set(rows, k, fmt, dev, at + start, at + off, at + off + ns if nv else None)
+            m._parts, m._buf = None, (buf, start, nd, off, ns)
+            out.append(m)
+        return out
 
     def _views(self):
         """(codes, scales, tensor scale) as tensors; cut from the allocation when first asked for."""
         if self._parts is None:
-            buf, nd, off, ns = self._buf
-            self._parts = buf[:nd], buf[off:off + ns], buf[off + ns:].view(torch.float32) if self.fmt == "nv" else None
+            buf, start, nd, off, ns = self._buf
+            self._parts = (buf[start:start + nd], buf[off:off + ns],
+                           buf[off + ns:off + ns + 8].view(torch.float32) if self.fmt == "nv" else None)
         return self._parts
 
     @property
@@ -192,7 +204,7 @@ def _source(x, fmt, along, out):
     rows, cols = x.shape
     shapes = [(rows, cols)] * want_c + [(cols, rows)] * want_r
     if out is None:
-        out = [Fp4Matrix.empty(*s, fmt, x.device) for s in shapes]
+        out = Fp4Matrix._alloc(shapes, fmt, x.device)
     else:
         out = list(out) if along == "both" else [out]
         if len(out) != len(shapes) or not all(isinstance(m, Fp4Matrix) for m in out):

@@ -54,7 +54,7 @@ def check_stored(m, q, amax_known=True):
 
 
 SHAPES = [(1, 1), (1, 2048), (2048, 1), (3, 17), (31, 33), (64, 48), (128, 128), (129, 257), (200, 31), (255, 130),
-          (300, 520), (1, 16), (7, 4000)]
+          (300, 520), (1, 16), (7, 4000), (8, 2048), (8, 2049), (16385, 1)]
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
