@@ -15,6 +15,8 @@
 #include "muon.h"
 #include "muon_internal.cuh"
 
+#include <atomic>
+
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
@@ -115,6 +117,18 @@ inline int device_sms(int dev) {
     }
   } all;
   return dev >= 0 && dev < 64 ? all.sms[dev] : 0;
+}
+
+// Host: let `kernel` use up to `bytes` of dynamic shared memory on device
+// `dev`; set once per kernel and device.
+template <auto kKernel>
+inline cudaError_t allow_smem(int dev, int bytes) {
+  static std::atomic<uint64_t> done{0};  // one bit per device
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // Byte of row r, block b within its atom.

@@ -555,7 +555,7 @@ bool encode_out(CUtensorMap* tm, const ProdArgs& g) {
 }
 
 template <int kCg, int kBn, bool kNv>
-muon_status_t launch_product(const muon_fp4_matrix_t& a, const muon_fp4_matrix_t& b, ProdArgs g, int sms,
+muon_status_t launch_product(const muon_fp4_matrix_t& a, const muon_fp4_matrix_t& b, ProdArgs g, int dev, int sms,
                              cudaStream_t st) {
   using C = Cfg<kCg, kBn, kNv>;
   CUtensorMap ma, mb, msa, msb, mo = {};
@@ -563,8 +563,7 @@ muon_status_t launch_product(const muon_fp4_matrix_t& a, const muon_fp4_matrix_t
       !encode_scales(&msb, b, kBn / 128) || (g.vec && !encode_out(&mo, g)))
     return MUON_ERR_CUDA;
   auto kernel = fp4_product_kernel<kCg, kBn, kNv>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
-    return MUON_ERR_CUDA;
+  if (allow_smem<fp4_product_kernel<kCg, kBn, kNv>>(dev, C::kSmem) != cudaSuccess) return MUON_ERR_CUDA;
   g.tiles_m = (g.m + kCg * 128 - 1) / (kCg * 128);
   g.tiles_n = (g.n + kBn - 1) / kBn;
   const int64_t tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
@@ -635,10 +634,10 @@ muon_status_t muon_fp4_product(const muon_fp4_matrix_t* a, const muon_fp4_matrix
   // pairs where there are enough 256 x 256 tiles for them, single CTAs below
   const int64_t pair_tiles = ((a->rows + 255) / 256) * ((b->rows + 255) / 256);
   if (pair_tiles >= sms / 4)
-    return nv ? launch_product<2, 256, true>(*a, *b, g, sms, st)
-              : launch_product<2, 256, false>(*a, *b, g, sms, st);
-  return nv ? launch_product<1, 128, true>(*a, *b, g, sms, st)
-            : launch_product<1, 128, false>(*a, *b, g, sms, st);
+    return nv ? launch_product<2, 256, true>(*a, *b, g, dev, sms, st)
+              : launch_product<2, 256, false>(*a, *b, g, dev, sms, st);
+  return nv ? launch_product<1, 128, true>(*a, *b, g, dev, sms, st)
+            : launch_product<1, 128, false>(*a, *b, g, dev, sms, st);
 }
 
 muon_status_t muon_fp4_get_status(void* stream) {

@@ -385,13 +385,13 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
 }
 
 template <bool kNv, int kNg, int kWarps>
-cudaError_t launch_rows_w(const RowsArgs& g, int ctas, int smem, cudaStream_t st) {
+cudaError_t launch_rows_w(const RowsArgs& g, int dev, int ctas, int smem, cudaStream_t st) {
   const int per = kWarps / g.ks;
   const int groups = ((g.n + 15) / 16 + per - 1) / per;
   const dim3 grid(groups < ctas ? groups : ctas, (g.t + g.tg - 1) / g.tg);
   auto kernel = fp4_rows_kernel<kNv, kNg, kWarps>;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<fp4_rows_kernel<kNv, kNg, kWarps>>(dev, kSmemMax);
     if (e != cudaSuccess) return e;
   }
   kernel<<<grid, 32 * kWarps, smem, st>>>(g);
@@ -405,7 +405,7 @@ cudaError_t launch_rows_w(const RowsArgs& g, int ctas, int smem, cudaStream_t st
 // 39.8 against 46.1 us); eight warps where X takes the shared memory.  (24
 // warps of 80 registers spill: t = 16 39.9 us.)
 template <bool kNv, int kNg>
-cudaError_t launch_rows(const RowsArgs& g, int sms, cudaStream_t st) {
+cudaError_t launch_rows(const RowsArgs& g, int dev, int sms, cudaStream_t st) {
   auto smem = [&](int warps) {
     return (g.t < g.tg ? g.t : g.tg) * g.xpitch + warps * (kDepth * kStepBytes + (g.ks > 1 ? 128 * kNg * 4 : 0));
   };
@@ -413,8 +413,8 @@ cudaError_t launch_rows(const RowsArgs& g, int sms, cudaStream_t st) {
   // fewer row tiles than 16 warps a SM take: CTAs of eight reach more SMs
   // (many rows of X are better copied by 16 warps)
   const bool few = static_cast<int64_t>((g.n + 15) / 16) * g.ks < 16 * static_cast<int64_t>(sms);
-  if ((kNg == 1 && (two || few)) || smem(16) > kSmemMax) return launch_rows_w<kNv, kNg, 8>(g, two ? 2 * sms : sms, smem(8), st);
-  return launch_rows_w<kNv, kNg, 16>(g, sms, smem(16), st);
+  if ((kNg == 1 && (two || few)) || smem(16) > kSmemMax) return launch_rows_w<kNv, kNg, 8>(g, dev, two ? 2 * sms : sms, smem(8), st);
+  return launch_rows_w<kNv, kNg, 16>(g, dev, sms, smem(16), st);
 }
 
 }  // namespace
@@ -465,8 +465,8 @@ extern "C" muon_status_t muon_fp4_rows_product(const void* x, int64_t t, int64_t
   while (g.ks < 8 && tiles * g.ks < 16 * static_cast<int64_t>(sms) && steps > 2 * g.ks) g.ks *= 2;
   const bool nv = w->format == MUON_FP4_NV;
   cudaError_t e;
-  if (ng == 1) e = nv ? launch_rows<true, 1>(g, sms, st) : launch_rows<false, 1>(g, sms, st);
-  else if (ng == 2) e = nv ? launch_rows<true, 2>(g, sms, st) : launch_rows<false, 2>(g, sms, st);
-  else e = nv ? launch_rows<true, 4>(g, sms, st) : launch_rows<false, 4>(g, sms, st);
+  if (ng == 1) e = nv ? launch_rows<true, 1>(g, dev, sms, st) : launch_rows<false, 1>(g, dev, sms, st);
+  else if (ng == 2) e = nv ? launch_rows<true, 2>(g, dev, sms, st) : launch_rows<false, 2>(g, dev, sms, st);
+  else e = nv ? launch_rows<true, 4>(g, dev, sms, st) : launch_rows<false, 4>(g, dev, sms, st);
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }

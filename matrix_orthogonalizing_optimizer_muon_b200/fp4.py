@@ -87,6 +87,15 @@ def _check_fmt(fmt: str) -> None:
         raise ValueError(f"fmt must be one of {sorted(_FMT)}, got {fmt!r}")
 
 
+def _part(t, name: str, dtype, n: int) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {n} elements, got {tuple(t.shape)}")
+
+
 class Fp4Matrix:
     """A 4-bit matrix [rows, k] on the device: codes `data` (uint8), `scales`
     (uint8) and, for "nv", `tensor_scale` (fp32: g and the largest magnitude),
@@ -99,19 +108,14 @@ class Fp4Matrix:
         if rows < 0 or k < 0 or rows > _MAX_DIM or k > _MAX_DIM:
             raise ValueError(f"a 4-bit matrix has 0 to 2^30 rows and columns, not {rows} x {k}")
         data_bytes, scale_bytes = _sizes(fmt, rows, k)
-        parts = [(data, "data", torch.uint8, data_bytes), (scales, "scales", torch.uint8, scale_bytes)]
+        _part(data, "data", torch.uint8, data_bytes)
+        _part(scales, "scales", torch.uint8, scale_bytes)
+        device = data.device
         if fmt == "nv":
-            parts.append((tensor_scale, "tensor_scale", torch.float32, 2))
-        for t, name, dt, n in parts:
-            if not isinstance(t, torch.Tensor) or not t.is_cuda:
-                raise TypeError(f"{name} must be a CUDA tensor")
-            if t.dtype != dt:
-                raise TypeError(f"{name} has dtype {t.dtype}, expected {dt}")
-            if not t.is_contiguous() or t.numel() != n:
-                raise ValueError(f"{name} must be contiguous with {n} elements, got {tuple(t.shape)}")
-            if t.device != data.device:
-                raise ValueError(f"{name} is on {t.device}, data on {data.device}")
-        self._set(rows, k, fmt, data.device, data.data_ptr(), scales.data_ptr(),
+            _part(tensor_scale, "tensor_scale", torch.float32, 2)
+        if scales.device != device or (fmt == "nv" and tensor_scale.device != device):
+            raise ValueError("data, scales and tensor_scale are on different devices")
+        self._set(rows, k, fmt, device, data.data_ptr(), scales.data_ptr(),
                   tensor_scale.data_ptr() if fmt == "nv" else None)
         self._parts = data, scales, tensor_scale if fmt == "nv" else None
 
@@ -172,22 +176,23 @@ class Fp4Matrix:
     def dequantize(self, dtype=torch.bfloat16, *, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """The values [rows, k] in bf16 or fp32 (or into `out`)."""
         with _on(self.device, stream):
-            if out is None:
-                if dtype not in _GDT:
-                    raise TypeError(f"dtype {dtype}: bf16 or fp32")
-                out = torch.empty(self.rows, self.k, dtype=dtype, device=self.device)
-            ld = _out_arg(out, (self.rows, self.k), self.device)
+            out, ld = _out(out, (self.rows, self.k), dtype, self.device)
             L.muon_fp4_dequantize(self._desc, out.data_ptr(), ld, _GDT[out.dtype], _current(self.device))
         return out
 
 
-def _out_arg(out, shape, device) -> int:
+def _out(out, shape, dtype, device):
+    """(the output, its row pitch): a new tensor of `dtype`, or a given one that fits."""
+    if out is None:
+        if dtype not in _GDT:
+            raise TypeError(f"output dtype {dtype}: bf16 or fp32")
+        return torch.empty(shape, dtype=dtype, device=device), shape[1]
     ld = _matrix_arg(out, "out")
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(shape)}")
+    if out.shape != shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
     if out.device != device:
         raise ValueError(f"out is on {out.device}, the operands on {device}")
-    return ld
+    return out, ld
 
 
 def _ways(along: str):
@@ -314,11 +319,7 @@ def fp4_product(a: Fp4Matrix, b: Fp4Matrix, *, out: torch.Tensor | None = None, 
     if accumulate and (out is None or out.dtype != torch.float32):
         raise ValueError("accumulate adds to an fp32 `out`")
     with _on(a.device, stream):
-        if out is None:
-            if out_dtype not in _GDT:
-                raise TypeError(f"out_dtype {out_dtype}: bf16 or fp32")
-            out = torch.empty(a.rows, b.rows, dtype=out_dtype, device=a.device)
-        ld = _out_arg(out, (a.rows, b.rows), a.device)
+        out, ld = _out(out, (a.rows, b.rows), out_dtype, a.device)
         L.muon_fp4_product(a._desc, b._desc, out.data_ptr(), ld, _GDT[out.dtype], 1 if accumulate else 0,
                            _current(a.device))
     return out
@@ -338,11 +339,7 @@ def fp4_rows_product(x: torch.Tensor, w: Fp4Matrix, *, out: torch.Tensor | None 
     if x.shape[0] > MAX_ROWS:
         raise ValueError(f"x has {x.shape[0]} rows, at most {MAX_ROWS} are taken: quantise it and use fp4_product")
     with _on(w.device, stream):
-        if out is None:
-            if out_dtype not in _GDT:
-                raise TypeError(f"out_dtype {out_dtype}: bf16 or fp32")
-            out = torch.empty(x.shape[0], w.rows, dtype=out_dtype, device=w.device)
-        ld = _out_arg(out, (x.shape[0], w.rows), w.device)
+        out, ld = _out(out, (x.shape[0], w.rows), out_dtype, w.device)
         L.muon_fp4_rows_product(x.data_ptr(), x.shape[0], ldx, w._desc, out.data_ptr(), ld, _GDT[out.dtype],
                                 _current(w.device))
     return out
