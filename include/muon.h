@@ -447,7 +447,7 @@ MUON_API void muon_entropy_destroy(muon_entropy_plan_t plan);
  *           blocks, the atoms in row-major order [ceil(rows / 128)]
  *           [ceil(k / (4 block))], 16-byte aligned: row r, block b is byte
  *           (r % 32) 16 + (r % 128 / 32) 4 + b % 4 of atom (r / 128, b / 4).
- *           Bytes of no row or block are 0.
+ *           Bytes of no row or block are 0, and so is bit 7 of an e4m3 byte.
  *   tensor_scale  NV: two floats, g and amax_matrix.  The products take any
  *           finite g (a checkpoint's tensor scale need not be a power of two).
  * ------------------------------------------------------------------------ */
@@ -508,7 +508,9 @@ typedef struct muon_fp4_plan_s* muon_fp4_plan_t;
 MUON_API muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs, int32_t n,
                                      int32_t values_dtype, void* stream);
 
-/* Quantise every source of the plan, asynchronously on `stream`.  Errors:
+/* Quantise every source of the plan, asynchronously on `stream`, in two
+ * launches (NV) or one.  A plan holds the largest magnitudes between them, so
+ * runs of one plan, replays of captured ones too, must not overlap.  Errors:
  * INVALID_ARG (NULL plan, or another device is current), CUDA. */
 MUON_API muon_status_t muon_fp4_run(muon_fp4_plan_t plan, void* stream);
 
@@ -522,7 +524,8 @@ MUON_API void muon_fp4_destroy(muon_fp4_plan_t plan);
 /* out [a.rows, b.rows] (row pitch ldo elements, out_dtype) = A B^T, or with
  * accumulate = 1 (fp32 only) out + A B^T, of two 4-bit matrices of one format
  * and one k, asynchronously on `stream`: 4-bit tensor-core products with fp32
- * sums, times g_A g_B (NV).  k = 0 gives zeros (out as it is with accumulate).
+ * sums, times g_A g_B (NV); with accumulate each element is added to once, in
+ * fp32, where it lies (an addend or sum below 2^-126 may count as 0).  k = 0 gives zeros (out as it is with accumulate).
  * Rows of padding between ldo and b.rows are not written.  A NaN scale makes
  * its row (A) or column (B) of out NaN.
  * The call uses no workspace; calls on several streams are independent.
@@ -543,8 +546,8 @@ MUON_API muon_status_t muon_fp4_rows_product(const void* x, int64_t t, int64_t l
 
 /* Synchronizes `stream`, then returns and clears the current device's sticky
  * status of the muon_fp4_product calls: MUON_OK, or MUON_ERR_TIMEOUT after a
- * device-side wait gave up (the outputs of that call are invalid).
- * CUDA errors: MUON_ERR_CUDA. */
+ * device-side wait gave up (the outputs of that call are invalid).  Not for a
+ * stream that is being captured.  CUDA errors: MUON_ERR_CUDA. */
 MUON_API muon_status_t muon_fp4_get_status(void* stream);
 
 #ifdef __cplusplus

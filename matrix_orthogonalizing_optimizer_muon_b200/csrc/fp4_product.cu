@@ -360,6 +360,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const float ga = fabsf(sa) < fabsf(sb) ? sa : sb, gb = fabsf(sa) < fabsf(sb) ? sb : sa;
     const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * (kBn / 2);
     uint8_t* stg = smem + C::kEpi + (warp - kEpi0) * kStagingBytes;
+    int turn = 0;
     uint32_t tphase = 0;
     for (int t = unit; t < ntiles; t += nunits) {
       const bool ready = wait_bounded(tfull_bar, tphase, abort_flag);
@@ -403,8 +404,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           const int col = col0 + c * 32;
           if (col >= g.n) continue;
           if (g.vec && (col + 32 <= g.n || g.n % 8 == 0)) {
-            uint8_t* blk = stg + (c & 1) * (kStagingBytes / 2);
-            if (lane == 0) bulk_wait_read_but<1>();  // the store before the last has read its half
+            // the halves take turns store by store (a ragged tile may store one
+            // block only): the store before the last has read this one
+            uint8_t* blk = stg + turn * (kStagingBytes / 2);
+            turn ^= 1;
+            if (lane == 0) bulk_wait_read_but<1>();
             __syncwarp();
 #pragma unroll
             for (int q = 0; q < 4; ++q)

@@ -236,6 +236,21 @@ def test_product_into_a_strided_output(fp4, m, ld, off, fmt):
         assert (big[keep] == 5.0).all()
 
 
+@pytest.mark.parametrize("m", [3000, 40000])
+@pytest.mark.parametrize("n", [264, 288, 392, 416, 520])
+def test_product_with_a_narrow_last_tile(fp4, m, n):
+    """Last column tiles of which a warp stores one block, many tiles a CTA:
+    every column as that of a product with the last columns alone."""
+    a = fp4.fp4_quantize(torch.randn(m, 96, device="cuda"), fmt="mx")
+    w = torch.randn(n, 96, device="cuda")
+    b = fp4.fp4_quantize(w, fmt="mx")
+    for dt in DT.values():
+        out = fp4.fp4_product(a, b, out_dtype=dt)
+        for lo in range(0, n, 128):
+            part = fp4.fp4_quantize(w[lo:lo + 128], fmt="mx")
+            assert torch.equal(out[:, lo:lo + 128], fp4.fp4_product(a, part, out_dtype=dt))
+
+
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
 @pytest.mark.parametrize("m", [200, 2400])
 def test_product_nan_scales_stay_in_their_row_and_column(fp4, m, fmt):
