@@ -171,21 +171,6 @@ __device__ __forceinline__ void e2m1_values8(uint32_t w, float s, float* v) {
   }
 }
 
-// Eight values to eight codes, v[0] in the lowest four bits: nearest, ties to
-// the even code, saturating at 6.
-__device__ __forceinline__ uint32_t e2m1_pack8(const float* v) {
-  uint32_t w;
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
-      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
-      : "=r"(w)
-      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
-  return w;
-}
-
 // The matrix's power of two: the least g = 2^e, e >= -100, with amax <= 2688 g,
 // so that the largest block scale amax / (6 g) is at most 448, e4m3's largest.
 // 2688 = 1.3125 * 2^11, so e follows from the bits of amax (a finite fp32).
@@ -197,12 +182,12 @@ __host__ __device__ __forceinline__ int tensor_exponent(uint32_t amax_bits) {
 }
 
 // Scale of one block from the bits of its largest magnitude (anything at or
-// above the bits of infinity says that the block holds a NaN or an infinity).
+// above the bits of infinity says that the block holds a NaN or an infinity;
+// the codes of such a block do not matter).
 struct BlockScale {
-  uint32_t byte;  // the scale byte
-  float d, r;     // NV: the scale and about its reciprocal (0, 0 for a zero scale)
-                  // MX: r alone, the exact reciprocal
-                  // (the codes of a block with a NaN scale do not matter)
+  uint32_t byte;       // the scale byte
+  uint64_t r, r_rest;  // the scale's reciprocal as a pair of equal floats: MX r alone, exact; NV rounded down,
+                       // and what is left of it (both 0 for a zero scale)
 };
 
 // A matrix's scale and what its blocks' scales are found with.
@@ -224,44 +209,78 @@ __device__ __forceinline__ float rcp_approx(float d) {
   return r;
 }
 
-// x / d from r, d's reciprocal to within two steps: the product is corrected
-// once by its remainder, which gives the quotient to within an fp32 rounding,
-// and exactly where it has few bits.  In this form a zero keeps its sign.
-__device__ __forceinline__ float quotient(float x, float d, float r) {
-  const float q = x * r;
-  return fmaf(-fmaf(q, d, -x), r, q);
+__device__ __forceinline__ uint64_t twice(float v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+  return r;
 }
 
 template <bool kNv>
 __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, const MatrixScale& m) {
   BlockScale b;
-  b.d = 0.0f;
   if (kNv) {
-    // amax / (6 g) is rounded twice, to fp32 and then to e4m3, with the result
+    // amax / (6 g), the product with the reciprocal corrected once by its
+    // remainder, is rounded twice, to fp32 and then to e4m3, with the result
     // of one rounding: a quotient by 6 g (significand 1.5) that is not itself
     // a midpoint of e4m3 (5 significant bits) lies more than half an fp32
     // step from every midpoint.
-    const bool bad = amax_bits >= 0x7F800000u;
-    b.byte = __nv_cvt_float_to_fp8(quotient(__uint_as_float(amax_bits), m.six, m.sixth), __NV_SATFINITE, __NV_E4M3);
-    if (bad) b.byte = 0x7Fu;
-    b.d = e4m3_value(b.byte) * m.g;  // exact: four significant bits; below 2^126
-    b.r = b.byte != 0u ? rcp_approx(b.d) : 0.0f;
+    const float x = __uint_as_float(amax_bits), q = x * m.sixth;
+    b.byte = __nv_cvt_float_to_fp8(fmaf(-fmaf(q, m.six, -x), m.sixth, q), __NV_SATFINITE, __NV_E4M3);
+    if (amax_bits >= 0x7F800000u) b.byte = 0x7Fu;
+    // 1 / d as r + rest, r rounded down so that neither is negative
+    const float d = e4m3_value(b.byte) * m.g;  // exact: four significant bits; below 2^126
+    const float a = rcp_approx(d);
+    const float r = __fmaf_rd(fmaf(-d, a, 1.0f), a, a);
+    const float rest = fmaf(-d, r, 1.0f) * r;
+    b.r = b.byte != 0u ? twice(r) : 0u;
+    b.r_rest = b.byte != 0u ? twice(rest) : 0u;
   } else {
     const int e = static_cast<int>(amax_bits >> 23) - 2;
     b.byte = e < 0 ? 0u : static_cast<uint32_t>(e);
-    b.r = __uint_as_float((254u - b.byte) << 23);
+    b.r = twice(__uint_as_float((254u - b.byte) << 23));
+    b.r_rest = 0u;
     if (amax_bits >= 0x7F800000u) b.byte = 255u;
   }
   return b;
 }
 
-// x divided by the block's scale, such that the rounding to e2m1 that follows
-// gives the code of the exact quotient.  MX: the product with a power of two
-// is exact.  NV: a quotient by a four-bit d that is no midpoint of e2m1 (three
-// significant bits) is more than half an fp32 step from every midpoint.
+// Two values divided by their block's scale.  MX: the product with a power of
+// two is exact.  NV: x r + x rest, one rounding of the quotient to within
+// 2^-46 of it, which is exact where the quotient has few bits and else on the
+// right side of every border: a quotient by a four-bit scale that is no
+// midpoint of e2m1 (three significant bits) is more than half an fp32 step
+// from every midpoint.  A zero keeps its sign, since r and rest are not
+// negative.  Both lanes in one instruction each (f32x2).
 template <bool kNv>
-__device__ __forceinline__ float scaled(float x, const BlockScale& b) {
-  return kNv ? quotient(x, b.d, b.r) : x * b.r;
+__device__ __forceinline__ uint64_t quotients(float x0, float x1, const BlockScale& b) {
+  uint64_t x, q;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
+  if (kNv) {
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(b.r_rest));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(x), "l"(b.r), "l"(q));
+  } else {
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(b.r));
+  }
+  return q;
+}
+
+// Eight values to eight codes, v[0] in the lowest four bits: quotients rounded
+// to nearest, ties to the even code, saturating at 6.
+template <bool kNv>
+__device__ __forceinline__ uint32_t codes8(const float* v, const BlockScale& b) {
+  uint64_t q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = quotients<kNv>(v[2 * i], v[2 * i + 1], b);
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .f32 x, y;\n\t"
+      "mov.b64 {x, y}, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b0, y, x;\n\t"
+      "mov.b64 {x, y}, %2;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, y, x;\n\t"
+      "mov.b64 {x, y}, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 b2, y, x;\n\t"
+      "mov.b64 {x, y}, %4;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, y, x;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "l"(q[0]), "l"(q[1]), "l"(q[2]), "l"(q[3]));
+  return w;
 }
 
 }  // namespace fp4

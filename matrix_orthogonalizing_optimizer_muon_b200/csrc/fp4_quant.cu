@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(kThreads) amax_kernel(const __grid_constant__ 
   if constexpr (kList) listed = items[ref.item];  // all of it at once
   const Item& it = kList ? listed : one;
   const int row0 = ref.ty * kTileR, col0 = ref.tx * kTile;
+  pdl_trigger();
   if (row0 >= it.rows) return;  // the tiles that only fill up scale atoms
   uint32_t a = 0u;
   if (it.vec) {
@@ -300,21 +301,6 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const __grid_constant__
   const bool inside = row0 + kTileR <= it.rows && col0 + kTile <= it.cols;
   const int half = ty & 1;  // of the 128 rows of an atom
   const int t = threadIdx.x;
-  MatrixScale g = {};
-  if (kNv) {
-    const uint32_t bits = !kList && it.amax == nullptr ? small_amax<T>(it) : *it.amax;
-    g = matrix_scale(bits);
-    if ((tx | ty | t) == 0) {
-      if (kCols) {
-        it.c.ts[0] = g.g;
-        it.c.ts[1] = __uint_as_float(bits);
-      }
-      if (kRows) {
-        it.r.ts[0] = g.g;
-        it.r.ts[1] = __uint_as_float(bits);
-      }
-    }
-  }
 
   // ---- by rows: units of 16 values, unit u = (row u / 8, columns 16 (u % 8))
   constexpr int kN = kUnits;
@@ -348,6 +334,24 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const __grid_constant__
       }
     }
   }
+  MatrixScale g = {};
+  if (kNv) {
+    // the pass before (which started after everything before it had ended) may
+    // still run while this tile is loaded; its maximum, and all writes, wait
+    pdl_wait();
+    const uint32_t bits = !kList && it.amax == nullptr ? small_amax<T>(it) : *it.amax;
+    g = matrix_scale(bits);
+    if ((tx | ty | t) == 0) {
+      if (kCols) {
+        it.c.ts[0] = g.g;
+        it.c.ts[1] = __uint_as_float(bits);
+      }
+      if (kRows) {
+        it.r.ts[0] = g.g;
+        it.r.ts[1] = __uint_as_float(bits);
+      }
+    }
+  }
   if (kCols) {
     const int c16 = t & 7;
     const int64_t byte = static_cast<int64_t>(col0) / 2 + c16 * 8;
@@ -360,10 +364,10 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const __grid_constant__
       const BlockScale bs = block_scale<kNv>(a, g);
       float v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = scaled<kNv>(value_at<T>(w[k], i), bs);
+      for (int i = 0; i < 16; ++i) v[i] = value_at<T>(w[k], i);
       if (inside || (row0 + r < it.rows && byte < it.c.pitch))
         *reinterpret_cast<uint2*>(out + static_cast<int64_t>(k * (kThreads / 8)) * it.c.pitch) =
-            make_uint2(e2m1_pack8(v), e2m1_pack8(v + 8));
+            make_uint2(codes8<kNv>(v, bs), codes8<kNv>(v + 8, bs));
       // [atom][r % 32][r / 32][block]: the tile's half of each 16 bytes
       const int b = kNv ? c16 : c16 >> 1;
       if (kNv || (c16 & 1) == 0) sc_c[(b >> 2) * 256 + (r & 31) * 8 + (r >> 5) * 4 + (b & 3)] = static_cast<uint8_t>(bs.byte);
@@ -427,8 +431,8 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const __grid_constant__
       for (int q = 0; q < kBlk / 16; ++q) {
         float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = scaled<kNv>(__uint_as_float(x[h][16 * q + i]), bs);
-        *reinterpret_cast<uint2*>(out + 8 * q) = make_uint2(e2m1_pack8(v), e2m1_pack8(v + 8));
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(x[h][16 * q + i]);
+        *reinterpret_cast<uint2*>(out + 8 * q) = make_uint2(codes8<kNv>(v, bs), codes8<kNv>(v + 8, bs));
       }
       // NV: the atom's four blocks; MX: two of them, [c % 32][c / 32][block]
       sc_r[(c & 31) * (kNv ? 16 : 8) + (c >> 5) * (kNv ? 4 : 2) + rb] = static_cast<uint8_t>(bs.byte);
@@ -463,19 +467,30 @@ struct Launch {
   dim3 grid;
   int dtype, format;
   bool cols, rows, vec;    // vec: every source's rows start on 16-byte boundaries
+  bool after_amax() const { return format == MUON_FP4_NV && !(one && one->amax == nullptr); }
 };
 
 template <typename T, bool kNv, bool kCols, bool kRows>
 cudaError_t launch_quant_t(const Launch& l, cudaStream_t st) {
-  const int smem = (kRows || !l.vec ? kTileR * Src<T>::kPitch : 0) + (kRows ? kTile * kStagePitch : 0);
-  if (l.one) quant_kernel<T, kNv, kCols, kRows, false><<<l.grid, kThreads, smem, st>>>(*l.one, nullptr, nullptr);
-  else quant_kernel<T, kNv, kCols, kRows, true><<<l.grid, kThreads, smem, st>>>(Item{}, l.items, l.tiles);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = l.grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (kRows || !l.vec ? kTileR * Src<T>::kPitch : 0) + (kRows ? kTile * kStagePitch : 0);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = l.after_amax() ? 1 : 0;
+  const Item* none = nullptr;
+  const TileRef* no_tiles = nullptr;
+  if (l.one) return cudaLaunchKernelEx(&cfg, quant_kernel<T, kNv, kCols, kRows, false>, *l.one, none, no_tiles);
+  return cudaLaunchKernelEx(&cfg, quant_kernel<T, kNv, kCols, kRows, true>, Item{}, l.items, l.tiles);
 }
 
 template <typename T, bool kNv>
 cudaError_t launch_quant_n(const Launch& l, cudaStream_t st) {
-  if (kNv && !(l.one && l.one->amax == nullptr)) {
+  if (l.after_amax()) {
     if (l.one) amax_kernel<T, false><<<l.grid, kThreads, 0, st>>>(*l.one, nullptr, nullptr);
     else amax_kernel<T, true><<<l.grid, kThreads, 0, st>>>(Item{}, l.items, l.tiles);
     const cudaError_t e = cudaGetLastError();
