@@ -450,6 +450,11 @@ MUON_API void muon_entropy_destroy(muon_entropy_plan_t plan);
  *           Bytes of no row or block are 0, and so is bit 7 of an e4m3 byte.
  *   tensor_scale  NV: two floats, g and amax_matrix.  The products take any
  *           finite g (a checkpoint's tensor scale need not be a power of two).
+ *
+ * Every call below can be captured in a CUDA graph, except the plan's set-up
+ * and the status read; the first call of a kind on a device loads its kernel
+ * and belongs before a capture.  Calls without a plan share no memory, so
+ * they may overlap on several streams and come from several host threads.
  * ------------------------------------------------------------------------ */
 typedef enum { MUON_FP4_NONE = -1, MUON_FP4_MX = 0, MUON_FP4_NV = 1 } muon_fp4_format_t;
 

@@ -22,8 +22,8 @@
 //                on 16-byte boundaries (TMA writes whole 16-byte pieces), by
 //                rows of the block.  Two
 //                accumulators and the scales do not fit into TMEM's 512
-//                columns, so bf16 outputs are packed in registers and the
-//                accumulator is released before any of them is stored.
+//                columns, so a warp takes its share into registers (packed, if
+//                bf16) and releases the accumulator before it stores any.
 #include "fp4.cuh"
 #include "tc_ptx.cuh"
 
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       uint32_t phase = 0, tphase = 0;
       bool issued = false, ok = true;
       for (int t = unit; t < ntiles && ok; t += nunits) {
-        ok = __all_sync(0xffffffffu, wait_bounded(tempty_bar, tphase ^ 1u, abort_flag));
+        ok = __all_sync(0xffffffffu, wait_hot(tempty_bar, tphase ^ 1u, abort_flag));
         if (!ok) break;
         tphase ^= 1u;
         tc_fence_after();
@@ -437,17 +437,19 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           }
         }
       } else {
-#pragma unroll 1
+        uint32_t v[kPer][32];
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) tmem_ld32(tq + c * 32, v[c]);
+        tmem_ld_wait();
+        release();
+        if (row0 >= g.m) continue;
+#pragma unroll
         for (int c = 0; c < kPer; ++c) {
-          uint32_t v[32];
-          tmem_ld32(tq + c * 32, v);
-          tmem_ld_wait();
-          if (c == kPer - 1) release();
           const int col = col0 + c * 32;
-          if (row0 >= g.m || col >= g.n) continue;
+          if (col >= g.n) continue;
           if (kNv) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * ga * gb);
+            for (int i = 0; i < 32; ++i) v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) * ga * gb);
           }
           if (lane == 0) bulk_wait_read();
           __syncwarp();
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
             for (int q = 0; q < 8; ++q)
               *reinterpret_cast<uint4*>(stg + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-                  make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                  make_uint4(v[c][4 * q], v[c][4 * q + 1], v[c][4 * q + 2], v[c][4 * q + 3]);
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             uint32_t* w = reinterpret_cast<uint32_t*>(stg);
             // word i of row r at column i ^ r: conflict-free both ways
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[lane * 32 + (i ^ lane)] = v[i];
+            for (int i = 0; i < 32; ++i) w[lane * 32 + (i ^ lane)] = v[c][i];
             __syncwarp();
             const int nr = min(32, g.m - row0);
             if (col + lane < g.n) {
