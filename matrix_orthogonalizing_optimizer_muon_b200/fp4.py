@@ -353,30 +353,56 @@ class Fp4Kept:
         self.xt, self.w = xt, w
 
 
+def _both(x, name: str, fmt: str, device, st: int):
+    """Both forms (along cols, along rows) of a matrix, on the current device and stream."""
+    ld = _matrix_arg(x, name)
+    rows, cols = x.shape
+    c, r = Fp4Matrix._alloc(((rows, cols), (cols, rows)), fmt, device)
+    L.muon_fp4_quantize(L.muon_fp4_source_t(x.data_ptr(), ld, rows, cols, _GDT[x.dtype], 0, c._desc, r._desc), st)
+    return c, r
+
+
+def _times(a: Fp4Matrix, b: Fp4Matrix, out, dtype, accumulate: bool, st: int):
+    """fp4_product of matrices that are known to fit, on the current device and stream."""
+    out, ld = _out(out, (a.rows, b.rows), dtype, a.device)
+    L.muon_fp4_product(a._desc, b._desc, out.data_ptr(), ld, _GDT[out.dtype], 1 if accumulate else 0, st)
+    return out
+
+
 def fp4_linear(x: torch.Tensor, w, *, fmt: str | None = None, out_dtype=torch.bfloat16, stream=None):
     """y = Q(x) Q(w) for x [T, K] and a weight w [K, N], Q the rounding to 4
     bits in blocks along the summed dimension.  w is a tensor, or the pair
     (along cols, along rows) that fp4_quantize or an Fp4Plan made of it with
     along="both".  Returns (y [T, N], what fp4_linear_backward needs)."""
+    _matrix_arg(x, "x")
+    device = x.device
     if isinstance(w, torch.Tensor):
         fmt = fmt or "nv"
-        w_cols, w_rows = fp4_quantize(w, fmt=fmt, along="both", stream=stream)
+        _check_fmt(fmt)
+        _matrix_arg(w, "w")
+        shape, w_device = w.shape, w.device
     else:
         if not (isinstance(w, (tuple, list)) and len(w) == 2 and all(isinstance(m, Fp4Matrix) for m in w)):
             raise TypeError("w must be a tensor or the pair (along cols, along rows) of its 4-bit forms")
         w_cols, w_rows = w
-        if w_cols.shape != w_rows.shape[::-1] or w_cols.fmt != w_rows.fmt:
+        if w_cols.shape != w_rows.shape[::-1] or w_cols.fmt != w_rows.fmt or w_cols.device != w_rows.device:
             raise ValueError(f"the forms of w do not belong together: {w_cols.fmt} {w_cols.shape}, "
                              f"{w_rows.fmt} {w_rows.shape}")
         if fmt is not None and fmt != w_cols.fmt:
             raise ValueError(f"w is in format {w_cols.fmt}, not {fmt}")
-        fmt = w_cols.fmt
-    _matrix_arg(x, "x")
-    if x.shape[1] != w_cols.rows:
-        raise ValueError(f"x has {x.shape[1]} columns, w has {w_cols.rows} rows")
-    xq, xt = fp4_quantize(x, fmt=fmt, along="both", stream=stream)
-    y = fp4_product(xq, w_rows, out_dtype=out_dtype, stream=stream)
-    return y, Fp4Kept(xt, w_cols)
+        fmt, shape, w_device = w_cols.fmt, w_cols.shape, w_cols.device
+    if x.shape[1] != shape[0]:
+        raise ValueError(f"x has {x.shape[1]} columns, w has {shape[0]} rows")
+    if w_device != device:
+        raise ValueError(f"x is on {device}, w on {w_device}")
+    if out_dtype not in _GDT:
+        raise TypeError(f"out_dtype {out_dtype}: bf16 or fp32")
+    with _on(device, stream):
+        st = _current(device)
+        if isinstance(w, torch.Tensor):
+            w_cols, w_rows = _both(w, "w", fmt, device, st)
+        xq, xt = _both(x, "x", fmt, device, st)
+        return _times(xq, w_rows, None, out_dtype, False, st), Fp4Kept(xt, w_cols)
 
 
 def fp4_linear_backward(kept: Fp4Kept, dy: torch.Tensor, *, dw: torch.Tensor | None = None, accumulate: bool = False,
@@ -388,16 +414,23 @@ def fp4_linear_backward(kept: Fp4Kept, dy: torch.Tensor, *, dw: torch.Tensor | N
     accumulate=True added to (fp32), which gathers several micro-batches."""
     if not isinstance(kept, Fp4Kept):
         raise TypeError("kept must come from fp4_linear")
-    tokens, n = kept.xt.k, kept.w.k
+    tokens, n, device, fmt = kept.xt.k, kept.w.k, kept.w.device, kept.w.fmt
     _matrix_arg(dy, "dy")
     if tuple(dy.shape) != (tokens, n):
         raise ValueError(f"dy has shape {tuple(dy.shape)}, expected {(tokens, n)}")
-    if accumulate and dw is None:
-        raise ValueError("accumulate adds to a given dw")
-    dyq, dyt = fp4_quantize(dy, fmt=kept.w.fmt, along="both", stream=stream)
-    dx = fp4_product(dyq, kept.w, out_dtype=dx_dtype, stream=stream)
-    dw = fp4_product(kept.xt, dyt, out=dw, out_dtype=torch.float32, accumulate=accumulate, stream=stream)
-    return dx, dw
+    if dy.device != device:
+        raise ValueError(f"dy is on {dy.device}, the layer on {device}")
+    if accumulate and (dw is None or dw.dtype != torch.float32):
+        raise ValueError("accumulate adds to a given fp32 dw")
+    if dw is not None:
+        _out(dw, (kept.xt.rows, n), None, device)  # refused before anything is enqueued
+    if dx_dtype not in _GDT:
+        raise TypeError(f"dx_dtype {dx_dtype}: bf16 or fp32")
+    with _on(device, stream):
+        st = _current(device)
+        dyq, dyt = _both(dy, "dy", fmt, device, st)
+        dx = _times(dyq, kept.w, None, dx_dtype, False, st)
+        return dx, _times(kept.xt, dyt, dw, torch.float32, accumulate, st)
 
 
 def fp4_status(stream=None) -> int:

@@ -575,6 +575,16 @@ def test_front_end_refusals(fp4):
         fp4.fp4_linear_backward(kept, x[:32])
     with pytest.raises(ValueError):
         fp4.fp4_linear_backward(kept, x, accumulate=True)
+    with pytest.raises(ValueError):
+        fp4.fp4_linear_backward(kept, x, dw=torch.empty(64, 64, dtype=torch.bfloat16, device="cuda"), accumulate=True)
+    with pytest.raises(ValueError):
+        fp4.fp4_linear_backward(kept, x, dw=torch.empty(64, 63, device="cuda"))
+    with pytest.raises(TypeError):
+        fp4.fp4_linear_backward(kept, x, dx_dtype=torch.float16)
+    with pytest.raises(TypeError):
+        fp4.fp4_linear(x, x, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        fp4.fp4_linear(x, x, fmt="int4")
     from matrix_orthogonalizing_optimizer_muon_b200 import _lib as L
     with pytest.raises(L.MuonError):  # the output over an operand
         short = fp4.fp4_quantize(x[:4])
