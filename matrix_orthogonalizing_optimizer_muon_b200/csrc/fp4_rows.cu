@@ -60,6 +60,23 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// the same from zero
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// Four 8 x 16-byte matrices whose rows lie one after another: word t4 of row gr of each.
+__device__ __forceinline__ void load_words(uint32_t (&w)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr)
+               : "memory");
+}
+
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -266,9 +283,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
             // blocks 2 t4 and 2 t4 + 1 of the step's eight: half a word
             sw[h] = *reinterpret_cast<const unsigned short*>(st + 1024 + (h * 16 + (t4 >> 1) * 8 + gr) * 4 + (t4 & 1) * 2);
           } else {
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-              w[h][b] = *reinterpret_cast<const uint32_t*>(st + h * 512 + b * 128 + gr * 16 + t4 * 4);
+            load_words(w[h], ring_s + static_cast<uint32_t>(d * kStepBytes + h * 512 + lane * 16));
             sw[h] = *reinterpret_cast<const uint32_t*>(st + 1024 + (h * 16 + gr) * 4);
           }
         }
@@ -316,8 +331,8 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
               mma16816(acc[q], lo[0], hi[0], lo[1], hi[1], x.x, x.y);
               mma16816(acc[q], lo[2], hi[2], lo[3], hi[3], x.z, x.w);
             } else {
-              float d4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              mma16816(d4, lo[0], hi[0], lo[1], hi[1], x.x, x.y);
+              float d4[4];
+              mma16816_first(d4, lo[0], hi[0], lo[1], hi[1], x.x, x.y);
               mma16816(d4, lo[2], hi[2], lo[3], hi[3], x.z, x.w);
               acc[q][0] = fmaf(s0, d4[0], acc[q][0]);
               acc[q][1] = fmaf(s0, d4[1], acc[q][1]);
