@@ -473,11 +473,19 @@ extern "C" muon_status_t muon_fp4_rows_product(const void* x, int64_t t, int64_t
   int ng = t <= 8 ? 1 : t <= 16 ? 2 : 4;
   while (ng > 1 && 8 * ng * g.xpitch > kXBudget) ng /= 2;
   g.tg = 8 * ng;
-  // k split: until the row tiles give every warp of the GPU one, or a warp has only two steps left
+  // k split: the fewest steps of a warp when 16 warps a SM take the row tiles in
+  // rounds, a reduction counted as a step
   const int64_t tiles = (w->rows + 15) / 16;
   const int steps = (g.kc + kStepK - 1) / kStepK;
-  g.ks = 1;
-  while (g.ks < 8 && tiles * g.ks < 16 * static_cast<int64_t>(sms) && steps > 2 * g.ks) g.ks *= 2;
+  int64_t best = 0;
+  for (int ks = 1; ks <= 8; ks *= 2) {
+    const int64_t rounds = (tiles * ks + 16 * sms - 1) / (16 * sms);
+    const int64_t cost = rounds * ((steps + ks - 1) / ks + (ks > 1 ? 1 : 0));
+    if (ks == 1 || cost < best) {
+      best = cost;
+      g.ks = ks;
+    }
+  }
   const bool nv = w->format == MUON_FP4_NV;
   cudaError_t e;
   if (ng == 1) e = nv ? launch_rows<true, 1>(g, dev, sms, st) : launch_rows<false, 1>(g, dev, sms, st);
