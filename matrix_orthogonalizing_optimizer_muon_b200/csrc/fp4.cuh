@@ -18,7 +18,6 @@
 #include <atomic>
 
 #include <cuda_fp16.h>
-#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
 namespace muon {
