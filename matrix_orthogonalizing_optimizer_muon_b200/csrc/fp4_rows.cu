@@ -17,11 +17,16 @@
 //      be outside fp16's range, so the products of a block are summed from
 //      zero (its 32 values are exactly two MMAs) and scaled in fp32.
 //   X  is held in shared memory as fp16, each row times its own power of two
-//      that puts its largest magnitude into [2^14, 2^15).  A bf16 has 8
-//      significant bits, so values down to 2^-32 of the largest stay exact and
-//      smaller ones are off by at most 2^-39 of it, below the fp32 sums'
-//      rounding; the power is undone at the end.  A row's result so does not
-//      depend on the other rows.
+//      that puts its largest magnitude into [2^14, 2^15); the power is undone
+//      at the end, so a row's result does not depend on the other rows.  A bf16
+//      has 8 significant bits and an fp16 goes down to 2^-24, so the values
+//      within 32 exponents of the largest are exact.  A CTA that finds one
+//      below (an output whose codes are zero under the larger values is made
+//      of such alone) takes X in parts instead, 32 exponents each with a power
+//      of two of its own, and multiplies W by one part after the other: eight
+//      cover all of bf16.  (bf16 operands would need no powers of two, but a
+//      code becomes a bf16 in about five instructions a pair instead of two,
+//      in a kernel that its instructions bound.)
 // Sums are fp32 in a fixed order.  KS warps split the k of a row tile where
 // there are too few row tiles to fill the GPU, and add up through shared
 // memory.
@@ -38,6 +43,7 @@ constexpr int kStepBytes = 1024 + 128;  // codes of 16 rows, then 8 bytes of sca
 constexpr int kMaxK = 10240;         // k of X in shared memory at a time
 constexpr int kXBudget = 164 * 1024; // bytes of it
 constexpr int kSmemMax = 226 * 1024;
+constexpr int kWindowLog = 5, kWindow = 1 << kWindowLog;  // exponents of X that one fp16 copy holds exactly
 constexpr int kMxShift = 16;         // MX scales are taken times 2^-16, so that a sum of scaled products
                                      // overflows only where a block scale is above 2^121
 
@@ -89,13 +95,23 @@ __device__ __forceinline__ uint32_t e8m0_pair(uint32_t w) {
   return r;
 }
 
-// Exponent of the power of two that is taken out of a row of X with the
-// largest magnitude a (bits).  At least -126: below, the row's values are
+// Exponent of the power of two that is taken out of part `part` of a row of X
+// with the largest magnitude a (bits).  At least -126: below, the values are
 // multiples of 2^-133, times 2^126 multiples of 2^-7, exact in fp16 all the same.
-__device__ __forceinline__ int exponent_of(uint32_t a) {
-  return max(static_cast<int>(a >> 23) - 127 - 14, -126);
+__device__ __forceinline__ int exponent_of(uint32_t a, int part = 0) {
+  return max(static_cast<int>(a >> 23) - 127 - 14 - kWindow * part, -126);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+// Exponent field of a finite magnitude (bits); subnormals count as the least normal numbers.
+__device__ __forceinline__ int field_of(uint32_t a) { return max(static_cast<int>(a >> 23), 1); }
+
+// Two magnitudes (bf16 bits) less 2^15 + 1 each, as signed halves: a zero wraps
+// to the largest, so a minimum is that of the values that are not zero.
+__device__ __forceinline__ uint32_t wrapped(uint32_t two) { return (two & 0x7FFF7FFFu) + 0x7FFF7FFFu; }
+// The lesser half, as its bf16 bits again (2^16 for a zero).
+__device__ __forceinline__ int least_half(uint32_t w) {
+  return min(static_cast<int>(w) >> 16, static_cast<int>(w << 16) >> 16) + 0x8001;
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   // the rest of the 16 bytes is filled with zeros
@@ -103,6 +119,262 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// true if the lesser of `least` (wrapped) lies kWindow exponents or more below a
+__device__ __forceinline__ bool spread(uint32_t a, uint32_t least) {
+  return field_of(a) - (least_half(least) >> 7) >= kWindow;
+}
+
+// Where 16-byte piece p of a row of X lies: within a step of 128 the pieces lie
+// in the order in which the four threads of a row take them, NV thread t4's
+// i-th piece (8 values of its 32) at 4 i + t4, MX in order.
+template <bool kNv>
+__device__ __forceinline__ int x_place(int p) {
+  return (kNv ? (p & ~15) + (p & 3) * 4 + ((p >> 2) & 3) : p) * 16;
+}
+
+// Eight values of a row of X with kn of them that starts anywhere; zeros past its end.
+__device__ __forceinline__ void x_piece(const unsigned short* src, int p, int kn, uint32_t (&v)[4]) {
+  if ((reinterpret_cast<uintptr_t>(src) & 15) == 0 && p * 8 + 8 <= kn) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(src) + p);
+    v[0] = q.x;
+    v[1] = q.y;
+    v[2] = q.z;
+    v[3] = q.w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned short* e = src + p * 8 + 2 * i;
+    const uint32_t lo = p * 8 + 2 * i < kn ? __ldg(e) : 0u, hi = p * 8 + 2 * i + 1 < kn ? __ldg(e + 1) : 0u;
+    v[i] = lo | (hi << 16);
+  }
+}
+
+// Stages part `part` of X of [k0, k0 + kc); finds the rows' ranges first when
+// that is the first part.
+template <bool kNv, int kNg, int kWarps>
+__device__ __forceinline__ void stage_part(const RowsArgs& g, int k0, int part, int t0, int nt, uint8_t* smem,
+                                           uint32_t* amax, int* amin, int* nparts) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kn = min(g.kc, g.k - k0);
+  const int pieces = (kn + kStepK - 1) / kStepK * (kStepK / 8);
+  auto row = [&](int r) {
+    return reinterpret_cast<const unsigned short*>(g.x) + static_cast<int64_t>(t0 + r) * g.ldx + k0;
+  };
+  if (part == 0) {
+    if (threadIdx.x == 0) *nparts = 1;
+    __syncthreads();
+#pragma unroll 1
+    for (int r = warp; r < nt; r += kWarps) {
+      uint32_t a = 0u, least = 0x7FFF7FFFu;
+#pragma unroll 4
+      for (int p = lane; p * 8 < kn; p += 32) {
+        uint32_t v[4];
+        x_piece(row(r), p, kn, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t lo = (v[i] << 16) & 0x7FFF0000u, hi = v[i] & 0x7FFF0000u;
+          a = max(a, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+          least = __vmins2(least, wrapped(v[i]));
+        }
+      }
+      a = __reduce_max_sync(0xffffffffu, a);
+      const int low = __reduce_min_sync(0xffffffffu, least_half(least));
+      if (lane == 0) {
+        amax[r] = a;
+        amin[r] = low;
+        // one part for a row of zeros or without a finite value
+        atomicMax(nparts, ((field_of(a) - max(low >> 7, 1)) >> kWindowLog) + 1);
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll 1
+  for (int r = warp; r < nt; r += kWarps) {
+    // the values whose exponents are in the part, zeros for the others; an
+    // infinity is in the first (no magnitude is at or above a NaN), a NaN in all
+    const float f = pow2(-exponent_of(amax[r], part));
+    const int top = field_of(amax[r]) - kWindow * part, bottom = top - kWindow + 1;
+    const float above = part == 0 ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(static_cast<uint32_t>(max(top + 1, 0)) << 23);
+    const float from = bottom > 1 ? __uint_as_float(static_cast<uint32_t>(bottom) << 23) : 0.0f;
+    auto in_part = [&](uint32_t v) {
+      const float x = __uint_as_float(v);
+      return !(fabsf(x) < from) && !(fabsf(x) >= above) ? x * f : 0.0f;
+    };
+#pragma unroll 4
+    for (int p = lane; p < pieces; p += 32) {
+      uint32_t v[4], h[4];
+      x_piece(row(r), p, kn, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 c = __floats2half2_rn(in_part(v[i] << 16), in_part(v[i] & 0xFFFF0000u));
+        h[i] = *reinterpret_cast<const uint32_t*>(&c);
+      }
+      *reinterpret_cast<uint4*>(smem + r * g.xpitch + x_place<kNv>(p)) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+  }
+}
+
+// One lane's outputs of a row tile: rows `row` and row + 8 of W.
+template <int kNg>
+__device__ __forceinline__ void store_rows(const RowsArgs& g, const float (&total)[kNg][4], int row, int t0, int nt, int t4) {
+#pragma unroll
+  for (int q = 0; q < kNg; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = row + (i >> 1) * 8, t = 8 * q + 2 * t4 + (i & 1);
+      if (r >= g.n || t >= nt) continue;
+      const int64_t at = static_cast<int64_t>(t0 + t) * g.ldo + r;
+      if (g.out_dtype == MUON_DT_BF16) static_cast<__nv_bfloat16*>(g.out)[at] = __float2bfloat16_rn(total[q][i]);
+      else static_cast<float*>(g.out)[at] = total[q][i];
+    }
+}
+
+// The row tiles of a CTA from group `grp` on, for an X whose rows spread over
+// more exponents than an fp16 holds: each row tile once for each part of X, its
+// sums in the order in which the kernel below adds them, so that a row of one
+// part has the same bits from both.  Out of line, W straight from memory and
+// steps not unrolled: the instructions of a call with few rows are a good part
+// of its time, and its common path keeps its own (inlined, or sharing its code
+// with the kernel, this cost that 5 to 13%).
+template <bool kNv, int kNg, int kWarps>
+__device__ __noinline__ void rows_in_parts(const RowsArgs g, int grp) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint32_t amax[8 * kNg];  // bits of the largest finite magnitude of each row of X
+  __shared__ int amin[8 * kNg];       // bf16 bits of the smallest that is not zero (2^16: none)
+  __shared__ int nparts;              // of the row with the most
+  asm volatile("cp.async.wait_all;" ::: "memory");  // the kernel's loads ahead
+  float* sums = reinterpret_cast<float*>(smem + min(g.tg, g.t) * g.xpitch + kWarps * kDepth * kStepBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gr = lane >> 2, t4 = lane & 3;
+  const int ks = warp % g.ks, rw = warp / g.ks, per = kWarps / g.ks;
+  const int t0 = blockIdx.y * g.tg;
+  const int nt = min(g.tg, g.t - t0);
+  const int ngroups = (g.n + 16 * per - 1) / (16 * per);
+  const int chunks = static_cast<int>(g.pitch >> 4), atoms = static_cast<int>(g.atoms);  // of a row
+  const float unit = kNv ? *g.ts : static_cast<float>(1 << kMxShift);
+#pragma unroll 1
+  for (; grp < ngroups; grp += gridDim.x) {
+    float total[kNg][4] = {};
+    const uint8_t *codes[2], *scales[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = min((grp * per + rw) * 16 + gr + 8 * h, g.n - 1);
+      codes[h] = g.data + static_cast<int64_t>(row) * g.pitch;
+      scales[h] = g.scales + static_cast<int64_t>(row >> 7) * g.atoms * kAtomBytes + atom_byte(row, 0);
+    }
+#pragma unroll 1
+    for (int k0 = 0; k0 < g.k; k0 += g.kc) {
+      const int steps = (min(g.kc, g.k - k0) + kStepK - 1) / kStepK;
+      int part = 0;
+#pragma unroll 1
+      do {
+        __syncthreads();
+        stage_part<kNv, kNg, kWarps>(g, k0, part, t0, nt, smem, amax, amin, &nparts);
+        __syncthreads();
+        float acc[kNg][4] = {};
+        uint32_t w[2][4], sw[2], next[2][4], snext[2];
+        auto fetch = [&](int j) {
+          const int at = k0 / kStepK + j;  // step of the row
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (kNv) {
+              const int piece = 4 * at + t4, atom = 2 * at + (t4 >> 1);
+              const uint4 v = piece < chunks ? __ldg(reinterpret_cast<const uint4*>(codes[h]) + piece) : make_uint4(0u, 0u, 0u, 0u);
+              next[h][0] = v.x;
+              next[h][1] = v.y;
+              next[h][2] = v.z;
+              next[h][3] = v.w;
+              snext[h] = atom < atoms ? __ldg(reinterpret_cast<const unsigned short*>(
+                                            scales[h] + static_cast<int64_t>(atom) * kAtomBytes + (t4 & 1) * 2))
+                                      : 0u;
+            } else {
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                next[h][b] = 4 * at + b < chunks ? __ldg(reinterpret_cast<const uint32_t*>(codes[h]) + (4 * at + b) * 4 + t4) : 0u;
+              snext[h] = at < atoms ? __ldg(reinterpret_cast<const uint32_t*>(scales[h] + static_cast<int64_t>(at) * kAtomBytes)) : 0u;
+            }
+          }
+        };
+        if (ks < steps) fetch(ks);
+#pragma unroll 1
+        for (int j = ks; j < steps; j += g.ks) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            sw[h] = snext[h];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) w[h][b] = next[h][b];
+          }
+          if (j + g.ks < steps) fetch(j + g.ks);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            uint32_t lo[4], hi[4];
+            e2m1_expand8(w[0][b], lo);
+            e2m1_expand8(w[1][b], hi);
+            float s[2] = {};
+            if (kNv) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const __half_raw r = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(sw[h] >> (b >> 1) * 8), __NV_E4M3);
+                const uint32_t two = r.x * 0x10001u;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) (h ? hi : lo)[p] = mul2((h ? hi : lo)[p], two);
+              }
+            } else {
+              constexpr float kDown = 1.0f / (1 << kMxShift);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) s[h] = e8m0_value((sw[h] >> b * 8) & 255u) * kDown;
+            }
+#pragma unroll
+            for (int q = 0; q < kNg; ++q) {
+              const uint4 x = *reinterpret_cast<const uint4*>(smem + min(8 * q + gr, nt - 1) * g.xpitch + t4 * 16 +
+                                                              j * (kStepK * 2) + b * 64);
+              if (kNv) {
+                mma16816(acc[q], lo[0], hi[0], lo[1], hi[1], x.x, x.y);
+                mma16816(acc[q], lo[2], hi[2], lo[3], hi[3], x.z, x.w);
+              } else {
+                float d4[4];
+                mma16816_first(d4, lo[0], hi[0], lo[1], hi[1], x.x, x.y);
+                mma16816(d4, lo[2], hi[2], lo[3], hi[3], x.z, x.w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[q][i] = fmaf(s[i >> 1], d4[i], acc[q][i]);
+              }
+            }
+          }
+        }
+        // undo the part's powers of two, the factor that shrinks first
+#pragma unroll
+        for (int q = 0; q < kNg; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int e = exponent_of(amax[min(8 * q + 2 * t4 + (i & 1), nt - 1)], part);
+            total[q][i] += acc[q][i] * (e < 0 ? pow2(e) : unit) * (e < 0 ? unit : pow2(e));
+          }
+      } while (++part < nparts);
+    }
+    if (g.ks > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < kNg; ++q)
+        *reinterpret_cast<float4*>(sums + (warp * kNg + q) * 128 + lane * 4) =
+            make_float4(total[q][0], total[q][1], total[q][2], total[q][3]);
+      __syncthreads();
+      if (ks != 0) continue;
+#pragma unroll 1
+      for (int w = 1; w < g.ks; ++w)
+#pragma unroll
+        for (int q = 0; q < kNg; ++q) {
+          const float4 v = *reinterpret_cast<const float4*>(sums + ((warp + w) * kNg + q) * 128 + lane * 4);
+          total[q][0] += v.x;
+          total[q][1] += v.y;
+          total[q][2] += v.z;
+          total[q][3] += v.w;
+        }
+    }
+    store_rows(g, total, (grp * per + rw) * 16 + gr, t0, nt, t4);
+  }
 }
 
 template <bool kNv, int kNg, int kWarps>
@@ -157,11 +429,10 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
     scale += (kNv ? 2 : 1) * kAtomBytes * g.ks;
   };
 
-  // X of [k0, k0 + kc) as scaled fp16, zeros past the edges.  Within a step
-  // of 128 the 16-byte pieces lie in the order in which the four threads of a
-  // row take them: NV thread t4's i-th piece (8 values of its 32) at 4 i + t4,
-  // MX in order.
-  // Few rows are each spread over several warps.
+  // X of [k0, k0 + kc) as scaled fp16, zeros past the edges.  Few rows are each
+  // spread over several warps.  `exact` turns false if a value lies 32 exponents
+  // or more below its row's largest.
+  bool exact = true;
   auto stage = [&](int k0) {
     const int kn = min(g.kc, g.k - k0);
     const int pieces = (kn + kStepK - 1) / kStepK * (kStepK / 8);
@@ -183,16 +454,19 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
       }
       return q;
     };
+    uint32_t least = 0u;  // of the last row: a warp with a share of a row has no other
     if (threadIdx.x < 8 * kNg) amax[threadIdx.x] = 0u;
     __syncthreads();
     for (int r = first; r < nt; r += rstep) {
       const unsigned short* src = reinterpret_cast<const unsigned short*>(g.x) + static_cast<int64_t>(t0 + r) * g.ldx + k0;
       const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
       uint32_t a = 0u;  // two magnitudes
-#pragma unroll 8
+      least = 0x7FFF7FFFu;
+#pragma unroll 4
       for (int p = p0; p < pieces; p += pstep) {
         const uint4 q = piece(src, vec, p);
         a = __vmaxu2(__vmaxu2(a, q.x & 0x7FFF7FFFu), __vmaxu2(q.y & 0x7FFF7FFFu, __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu)));
+        least = __vmins2(__vmins2(least, wrapped(q.x)), __vmins2(wrapped(q.y), __vmins2(wrapped(q.z), wrapped(q.w))));
       }
       a = __reduce_max_sync(0xffffffffu, max(a & 0xFFFF0000u, a << 16));
       if (a >= 0x7F800000u) {  // a NaN or an infinity: the finite values alone set the power of two
@@ -209,6 +483,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
         a = __reduce_max_sync(0xffffffffu, a);
       }
       if (lane == 0) atomicMax(&amax[r], a);
+      if (wpr == 1 && spread(a, least)) exact = false;
     }
     __syncthreads();
     for (int r = first; r < nt; r += rstep) {
@@ -226,9 +501,9 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
           const __half2 c = __floats2half2_rn(__uint_as_float(v[i] << 16) * f, __uint_as_float(v[i] & 0xFFFF0000u) * f);
           h[i] = *reinterpret_cast<const uint32_t*>(&c);
         }
-        const int at = kNv ? (p & ~15) + (p & 3) * 4 + ((p >> 2) & 3) : p;
-        *reinterpret_cast<uint4*>(dst + at * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(dst + x_place<kNv>(p)) = make_uint4(h[0], h[1], h[2], h[3]);
       }
+      if (wpr > 1 && spread(amax[r], least)) exact = false;
     }
   };
 
@@ -258,7 +533,10 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
       if (npass > 1 || !staged) {  // behind the first loads of W
         __syncthreads();
         stage(k0);
-        __syncthreads();
+        if (__syncthreads_or(!exact)) {
+          rows_in_parts<kNv, kNg, kWarps>(g, grp);
+          return;
+        }
         staged = true;
       }
       float acc[kNg][4];
@@ -405,7 +683,7 @@ cudaError_t launch_rows_w(const RowsArgs& g, int dev, int ctas, int smem, cudaSt
   const int groups = ((g.n + 15) / 16 + per - 1) / per;
   const dim3 grid(groups < ctas ? groups : ctas, (g.t + g.tg - 1) / g.tg);
   auto kernel = fp4_rows_kernel<kNv, kNg, kWarps>;
-  if (smem > 48 * 1024) {
+  if (smem + 1024 > 48 * 1024) {  // with the static share
     const cudaError_t e = allow_smem<fp4_rows_kernel<kNv, kNg, kWarps>>(dev, kSmemMax);
     if (e != cudaSuccess) return e;
   }

@@ -1,0 +1,96 @@
+"""The 4-bit operators at the ends of their ranges: few-row products whose
+rows and scales spread over all of bf16 and e8m0."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.fp4_oracle as o
+from test_gpu_fp4 import check_rows
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fp4():
+    from matrix_orthogonalizing_optimizer_muon_b200 import fp4 as m
+    return m
+
+
+def matrix(fp4, codes, byte, fmt, g=1.0):
+    """(Fp4Matrix, its values in fp64) of given codes [rows, k] and scale bytes [rows, blocks]."""
+    q = o.Fp4(codes, byte, g, 0.0, fmt, codes.shape[1])
+    data, scales = q.stored()
+    ts = torch.tensor([g, 0.0], device="cuda") if fmt == "nv" else None
+    m = fp4.Fp4Matrix(*codes.shape, fmt, torch.from_numpy(data).cuda(), torch.from_numpy(scales).cuda(), ts)
+    return m, q.values()
+
+
+def ones(rows, k, fmt):
+    """Scale bytes of 1."""
+    return np.full((rows, -(-k // o.BLOCK[fmt])), 127 if fmt == "mx" else 0x38)
+
+
+def bf16(x):
+    t = torch.from_numpy(x.astype(np.float32)).cuda().to(torch.bfloat16)
+    return t, t.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_rows_product_keeps_a_value_far_below_the_largest(fp4, fmt):
+    """2^30 meets a zero code: what is left of the row is the result, to the bit."""
+    codes = np.array([[0, 2, 0, 2]])  # 0 and 1
+    w, w64 = matrix(fp4, codes, ones(1, 4, fmt), fmt)
+    x, x64 = bf16(np.array([[2.0 ** 30, 2.0 ** -10, -(2.0 ** 90), 0.0],
+                            [-(2.0 ** 127), 2.0 ** -133, 0.0, 0.0],
+                            [2.0 ** 22, 3 * 2.0 ** -20, 1.0, 2.0 ** -18]]))
+    got = fp4.fp4_rows_product(x, w, out_dtype=torch.float32).double().cpu().numpy()
+    assert np.array_equal(got, x64 @ w64.T)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("t,n,k", [(1, 40, 96), (3, 300, 2048), (7, 33, 1409), (12, 100, 512), (32, 70, 200), (5, 48, 10500)])
+def test_rows_product_of_rows_that_spread_over_the_whole_range(fp4, t, n, k, fmt):
+    """Every row's values lie in groups down to 2^-250 of its largest, and each
+    row of W is zero under all groups above one of its own: each output within
+    the fp32 bound of the products that it is made of, and a row alone gives
+    the bits that it gives among others."""
+    r = np.random.default_rng(t * 1000 + k)
+    groups = np.array([100, 60, 31, 1, -1, -30, -35, -70, -100])
+    at = r.integers(0, len(groups), k)
+    x64 = r.standard_normal((t, k)) * 2.0 ** groups[at]
+    x64[0] = r.standard_normal(k)              # an ordinary row among them
+    if t > 2:
+        x64[1] *= 2.0 ** -20
+        x64[2, at < 4] = 0.0
+    x, x64 = bf16(x64)
+    codes = r.integers(0, 16, (n, k))
+    codes[at[None, :] < r.integers(0, len(groups), n)[:, None]] = 0
+    byte = r.integers(110, 140, (n, -(-k // 32))) if fmt == "mx" else r.integers(1, 127, (n, -(-k // 16)))
+    w, w64 = matrix(fp4, codes, byte, fmt, 2.0 ** -6)
+    got = fp4.fp4_rows_product(x, w, out_dtype=torch.float32)
+    check_rows(got, x64, w64, torch.float32)
+    for i in {0, 1 % t, t - 1}:
+        assert torch.equal(fp4.fp4_rows_product(x[i:i + 1], w, out_dtype=torch.float32), got[i:i + 1])
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_rows_product_spread_rows_with_nan_and_infinity(fp4, fmt):
+    """A NaN or an infinity in a row of several parts stays in its row, and a NaN scale in its column."""
+    r = np.random.default_rng(5)
+    x, x64 = bf16(r.standard_normal((4, 256)) * 2.0 ** r.integers(-100, 100, 256))
+    codes = r.integers(1, 8, (40, 256))
+    byte = ones(40, 256, fmt)
+    w, w64 = matrix(fp4, codes, byte, fmt)
+    whole = fp4.fp4_rows_product(x, w, out_dtype=torch.float32)
+    check_rows(whole, x64, w64, torch.float32)
+    x[1, 100], x[3, 0] = float("nan"), float("inf")
+    got = fp4.fp4_rows_product(x, w, out_dtype=torch.float32)
+    assert torch.equal(got[0::2], whole[0::2])
+    assert torch.isnan(got[1]).all() and (got[3] == float("inf")).all()
+    byte[7, 3] = 255 if fmt == "mx" else 127
+    w, _ = matrix(fp4, codes, byte, fmt)
+    got = fp4.fp4_rows_product(x[::2].contiguous(), w, out_dtype=torch.float32)
+    assert torch.isnan(got[:, 7]).all()
+    keep = [j for j in range(40) if j != 7]
+    assert torch.equal(got[:, keep], whole[0::2][:, keep])
