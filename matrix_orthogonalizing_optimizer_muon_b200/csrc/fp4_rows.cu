@@ -15,7 +15,10 @@
 //      NV: times the block's scale, exactly (e2m1 x e4m3 has at most six
 //      significant bits within fp16's range).  MX: the exponent of a scale may
 //      be outside fp16's range, so the products of a block are summed from
-//      zero (its 32 values are exactly two MMAs) and scaled in fp32.
+//      zero (its 32 values are exactly two MMAs) and scaled in fp32, times
+//      2^30: a sum of 10240 products then neither overflows for scales below
+//      2^65 nor loses a bit for the least, whatever power of two X's row is to
+//      be given back.  Blocks with larger scales are summed apart, times 2^-31.
 //   X  is held in shared memory as fp16, each row times its own power of two
 //      that puts its largest magnitude into [2^14, 2^15); the power is undone
 //      at the end, so a row's result does not depend on the other rows.  A bf16
@@ -44,8 +47,8 @@ constexpr int kMaxK = 10240;         // k of X in shared memory at a time
 constexpr int kXBudget = 164 * 1024; // bytes of it
 constexpr int kSmemMax = 226 * 1024;
 constexpr int kWindowLog = 5, kWindow = 1 << kWindowLog;  // exponents of X that one fp16 copy holds exactly
-constexpr int kMxShift = 16;         // MX scales are taken times 2^-16, so that a sum of scaled products
-                                     // overflows only where a block scale is above 2^121
+constexpr int kMxBig = 192;          // MX scale bytes from here on (2^65) are summed apart
+constexpr int kMxUp = 30, kMxDown = 31;  // scales are taken times 2^30, the big ones times 2^-31
 
 struct RowsArgs {
   const __nv_bfloat16* x;
@@ -88,11 +91,24 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Two e8m0 scales (of the low two bytes) as bf16 pairs' bits: 2^-127 and NaN included.
-__device__ __forceinline__ uint32_t e8m0_pair(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+// Bit 7 of every byte of four e8m0 scales that is kMxBig or more.
+__device__ __forceinline__ uint32_t mx_big(uint32_t w) { return w & (w << 1) & 0x80808080u; }
+// The four scales as the exponent fields that they are taken with, kMxUp above
+// their own (a byte 0 is 2^-127, so this holds for all): plain while none is
+// big, which then counts as 0.
+__device__ __forceinline__ uint32_t mx_up(uint32_t w) { return w + kMxUp * 0x01010101u; }
+__device__ __noinline__ uint32_t mx_up_mixed(uint32_t w) {
+  uint32_t r = 0u;
+#pragma unroll
+  for (int b = 0; b < 32; b += 8) {
+    const uint32_t byte = (w >> b) & 255u;
+    if (byte < kMxBig) r |= (byte + kMxUp) << b;
+  }
   return r;
+}
+// Scale b of them.
+__device__ __forceinline__ float mx_scale(uint32_t up, int b) {
+  return __uint_as_float((b < 3 ? up << (23 - 8 * b) : up >> 1) & 0x7F800000u);
 }
 
 // Exponent of the power of two that is taken out of part `part` of a row of X
@@ -102,6 +118,11 @@ __device__ __forceinline__ int exponent_of(uint32_t a, int part = 0) {
   return max(static_cast<int>(a >> 23) - 127 - 14 - kWindow * part, -126);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+// v 2^e for -252 <= e <= 254, in two steps the same way.
+__device__ __forceinline__ float times_pow2(float v, int e) {
+  const int h = e >> 1;
+  return v * pow2(h) * pow2(e - h);
+}
 // Exponent field of a finite magnitude (bits); subnormals count as the least normal numbers.
 __device__ __forceinline__ int field_of(uint32_t a) { return max(static_cast<int>(a >> 23), 1); }
 
@@ -232,13 +253,68 @@ __device__ __forceinline__ void store_rows(const RowsArgs& g, const float (&tota
     }
 }
 
+// MX: the sums of a warp's row tile (its lane's rows `row` and row + 8 of W)
+// over the blocks with big scales, times 2^-31; X of [k0, k0 + kc) is in shared
+// memory.  Rarely called, so out of line.
+template <int kNg>
+__device__ __noinline__ void big_scales(const RowsArgs g, int row, int k0, int ks, int nt, float* sums) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 31, gr = lane >> 2, t4 = lane & 3;
+  const int steps = (min(g.kc, g.k - k0) + kStepK - 1) / kStepK;
+  const int chunks = static_cast<int>(g.pitch >> 4), atoms = static_cast<int>(g.atoms);
+  float acc[kNg][4] = {};
+#pragma unroll 1
+  for (int j = ks; j < steps; j += g.ks) {
+    const int at = k0 / kStepK + j;  // step of the row, and its scale atom
+    uint32_t w[2][4], sw[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = min(row + 8 * h, g.n - 1);
+      sw[h] = at < atoms ? __ldg(reinterpret_cast<const uint32_t*>(
+                               g.scales + (static_cast<int64_t>(r >> 7) * g.atoms + at) * kAtomBytes + atom_byte(r, 0)))
+                         : 0u;
+      const uint32_t* codes = reinterpret_cast<const uint32_t*>(g.data + static_cast<int64_t>(r) * g.pitch) + t4;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) w[h][b] = 4 * at + b < chunks ? __ldg(codes + (4 * at + b) * 4) : 0u;
+    }
+    if (!__any_sync(0xffffffffu, (mx_big(sw[0]) | mx_big(sw[1])) != 0u)) continue;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      uint32_t lo[4], hi[4];
+      e2m1_expand8(w[0][b], lo);
+      e2m1_expand8(w[1][b], hi);
+      float s[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t byte = (sw[h] >> 8 * b) & 255u;
+        s[h] = byte == 255u ? __uint_as_float(0x7FFFFFFFu) : byte >= kMxBig ? __uint_as_float((byte - kMxDown) << 23) : 0.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < kNg; ++q) {
+        const uint4 x =
+            *reinterpret_cast<const uint4*>(smem + min(8 * q + gr, nt - 1) * g.xpitch + t4 * 16 + j * (kStepK * 2) + b * 64);
+        float d4[4];
+        mma16816_first(d4, lo[0], hi[0], lo[1], hi[1], x.x, x.y);
+        mma16816(d4, lo[2], hi[2], lo[3], hi[3], x.z, x.w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[q][i] = fmaf(s[i >> 1], d4[i], acc[q][i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kNg; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[4 * q + i] = acc[q][i];
+}
+
 // The row tiles of a CTA from group `grp` on, for an X whose rows spread over
-// more exponents than an fp16 holds: each row tile once for each part of X, its
-// sums in the order in which the kernel below adds them, so that a row of one
-// part has the same bits from both.  Out of line, W straight from memory and
-// steps not unrolled: the instructions of a call with few rows are a good part
-// of its time, and its common path keeps its own (inlined, or sharing its code
-// with the kernel, this cost that 5 to 13%).
+// more exponents than an fp16 holds, and for big MX scales: each row tile once
+// for each part of X, its sums in the order in which the kernel below adds
+// them, so that a row of one part has the same bits from both.  Out of line, W
+// straight from memory and steps not unrolled: the instructions of a call with
+// few rows are a good part of its time, and its common path keeps its own
+// (inlined, or sharing its code with the kernel, this cost that 5 to 13%).
+// Two parts take two to five times as long as one in the kernel.
 template <bool kNv, int kNg, int kWarps>
 __device__ __noinline__ void rows_in_parts(const RowsArgs g, int grp) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -254,7 +330,7 @@ __device__ __noinline__ void rows_in_parts(const RowsArgs g, int grp) {
   const int nt = min(g.tg, g.t - t0);
   const int ngroups = (g.n + 16 * per - 1) / (16 * per);
   const int chunks = static_cast<int>(g.pitch >> 4), atoms = static_cast<int>(g.atoms);  // of a row
-  const float unit = kNv ? *g.ts : static_cast<float>(1 << kMxShift);
+  const float unit = kNv ? *g.ts : 1.0f;
 #pragma unroll 1
   for (; grp < ngroups; grp += gridDim.x) {
     float total[kNg][4] = {};
@@ -275,7 +351,7 @@ __device__ __noinline__ void rows_in_parts(const RowsArgs g, int grp) {
         stage_part<kNv, kNg, kWarps>(g, k0, part, t0, nt, smem, amax, amin, &nparts);
         __syncthreads();
         float acc[kNg][4] = {};
-        uint32_t w[2][4], sw[2], next[2][4], snext[2];
+        uint32_t w[2][4], sw[2], next[2][4], snext[2], big = 0u;
         auto fetch = [&](int j) {
           const int at = k0 / kStepK + j;  // step of the row
 #pragma unroll
@@ -308,6 +384,13 @@ __device__ __noinline__ void rows_in_parts(const RowsArgs g, int grp) {
             for (int b = 0; b < 4; ++b) w[h][b] = next[h][b];
           }
           if (j + g.ks < steps) fetch(j + g.ks);
+          if (!kNv) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              big |= mx_big(sw[h]);
+              sw[h] = mx_up_mixed(sw[h]);
+            }
+          }
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             uint32_t lo[4], hi[4];
@@ -323,9 +406,8 @@ __device__ __noinline__ void rows_in_parts(const RowsArgs g, int grp) {
                 for (int p = 0; p < 4; ++p) (h ? hi : lo)[p] = mul2((h ? hi : lo)[p], two);
               }
             } else {
-              constexpr float kDown = 1.0f / (1 << kMxShift);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) s[h] = e8m0_value((sw[h] >> b * 8) & 255u) * kDown;
+              for (int h = 0; h < 2; ++h) s[h] = mx_scale(sw[h], b);
             }
 #pragma unroll
             for (int q = 0; q < kNg; ++q) {
@@ -350,8 +432,19 @@ __device__ __noinline__ void rows_in_parts(const RowsArgs g, int grp) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int e = exponent_of(amax[min(8 * q + 2 * t4 + (i & 1), nt - 1)], part);
-            total[q][i] += acc[q][i] * (e < 0 ? pow2(e) : unit) * (e < 0 ? unit : pow2(e));
+            if (kNv) total[q][i] += acc[q][i] * (e < 0 ? pow2(e) : unit) * (e < 0 ? unit : pow2(e));
+            else total[q][i] += times_pow2(acc[q][i], e - kMxUp);
           }
+        if (!kNv && __any_sync(0xffffffffu, big != 0u)) {
+          float more[4 * kNg];
+          big_scales<kNg>(g, (grp * per + rw) * 16 + gr, k0, ks, nt, more);
+#pragma unroll
+          for (int q = 0; q < kNg; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              total[q][i] += times_pow2(more[4 * q + i],
+                                        exponent_of(amax[min(8 * q + 2 * t4 + (i & 1), nt - 1)], part) + kMxDown);
+        }
       } while (++part < nparts);
     }
     if (g.ks > 1) {
@@ -512,8 +605,9 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
   int xrow[kNg];
 #pragma unroll
   for (int q = 0; q < kNg; ++q) xrow[q] = min(8 * q + gr, nt - 1) * g.xpitch + t4 * 16;
-  const float unit = kNv ? *g.ts : static_cast<float>(1 << kMxShift);
+  const float unit = kNv ? *g.ts : 1.0f;
   bool staged = false;
+  uint32_t big = 0u;  // MX: scales that this kernel counts as 0 were met
   for (int grp = blockIdx.x; grp < ngroups; grp += gridDim.x) {
     float total[kNg][4];
 #pragma unroll
@@ -577,12 +671,11 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
             sc[h][1] = __byte_perm(both, both, 0x3232);
           }
         }
-        uint32_t m0[2] = {0u, 0u}, m1[2] = {0u, 0u};
         if (!kNv) {
-          m0[0] = e8m0_pair(sw[0]);
-          m0[1] = e8m0_pair(sw[0] >> 16);
-          m1[0] = e8m0_pair(sw[1]);
-          m1[1] = e8m0_pair(sw[1] >> 16);
+          const uint32_t some = mx_big(sw[0]) | mx_big(sw[1]);
+          big |= some;
+          sw[0] = some == 0u ? mx_up(sw[0]) : mx_up_mixed(sw[0]);
+          sw[1] = some == 0u ? mx_up(sw[1]) : mx_up_mixed(sw[1]);
         }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -597,10 +690,8 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
               hi[p] = mul2(hi[p], sc[1][b >> 1]);
             }
           } else {
-            constexpr float kDown = 1.0f / (1 << kMxShift);
-            const uint32_t w0 = m0[b >> 1], w1 = m1[b >> 1];
-            s0 = __uint_as_float((b & 1) ? (w0 & 0xFFFF0000u) : (w0 << 16)) * kDown;
-            s1 = __uint_as_float((b & 1) ? (w1 & 0xFFFF0000u) : (w1 << 16)) * kDown;
+            s0 = mx_scale(sw[0], b);
+            s1 = mx_scale(sw[1], b);
           }
 #pragma unroll
           for (int q = 0; q < kNg; ++q) {
@@ -630,16 +721,21 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
       for (int d = 0; d < kDepth - 1; ++d)
         if (i + d < ni) step(i + d, d);
       __syncwarp();  // the ring is read before the next pass or tile fills it
-      // undo X's powers of two; the factor that shrinks comes first, so that
-      // nothing passes fp32's range that the result does not pass
+      // undo X's powers of two; NV: the factor that shrinks comes first, so
+      // that nothing passes fp32's range that the result does not pass
 #pragma unroll
       for (int q = 0; q < kNg; ++q)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int e = exponent_of(amax[min(8 * q + 2 * t4 + j, nt - 1)]);
-          const float f0 = e < 0 ? pow2(e) : unit, f1 = e < 0 ? unit : pow2(e);
-          total[q][j] += acc[q][j] * f0 * f1;
-          total[q][j + 2] += acc[q][j + 2] * f0 * f1;
+          if (kNv) {
+            const float f0 = e < 0 ? pow2(e) : unit, f1 = e < 0 ? unit : pow2(e);
+            total[q][j] += acc[q][j] * f0 * f1;
+            total[q][j + 2] += acc[q][j + 2] * f0 * f1;
+          } else {
+            total[q][j] += times_pow2(acc[q][j], e - kMxUp);
+            total[q][j + 2] += times_pow2(acc[q][j + 2], e - kMxUp);
+          }
         }
     }
     if (g.ks > 1) {
@@ -675,6 +771,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
         else static_cast<float*>(g.out)[at] = v;
       }
   }
+  if (!kNv && __syncthreads_or(big != 0u)) rows_in_parts<kNv, kNg, kWarps>(g, blockIdx.x);  // all of them again
 }
 
 template <bool kNv, int kNg, int kWarps>

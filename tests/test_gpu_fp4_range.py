@@ -94,3 +94,47 @@ def test_rows_product_spread_rows_with_nan_and_infinity(fp4, fmt):
     assert torch.isnan(got[:, 7]).all()
     keep = [j for j in range(40) if j != 7]
     assert torch.equal(got[:, keep], whole[0::2][:, keep])
+
+
+@pytest.mark.parametrize("t,n,k", [(3, 200, 64), (9, 100, 4096), (32, 33, 500), (2, 40, 10400)])
+@pytest.mark.parametrize("spread", [0, 60])
+def test_rows_product_mx_over_the_whole_range_of_scales(fp4, t, n, k, spread):
+    """MX scales from 2^-127 to 2^127 with rows of X of any size (and, with
+    spread, of many sizes within): whatever is within fp32's range is within
+    the bound of its sum, and repeated calls give the same bits."""
+    r = np.random.default_rng(n + k)
+    nb = -(-k // 32)
+    centre = r.integers(0, 255, n)             # every row of W around a size of its own
+    centre[:4] = (0, 1, 253, 254)
+    byte = np.clip(centre[:, None] + r.integers(-6, 7, (n, nb)), 0, 254)
+    byte[4:n // 2] = r.integers(0, 255, (n // 2 - 4, nb)) # or all sizes in one row
+    codes = r.integers(0, 16, (n, k))
+    w, w64 = matrix(fp4, codes, byte, "mx")
+    e = np.linspace(-120, 120, t)[:, None] + r.integers(-spread, spread + 1, k)
+    x, x64 = bf16(np.clip(r.standard_normal((t, k)), -2, 2) * 2.0 ** np.clip(e, -130, 126))
+    got = fp4.fp4_rows_product(x, w, out_dtype=torch.float32)
+    s = np.abs(x64) @ np.abs(w64).T
+    fits = s < 2.0 ** 127
+    assert fits.any() and (s[fits] > 2.0 ** 100).any()
+    g64 = got.double().cpu().numpy()
+    tol = (k + 4) * 2.0 ** -24 * s + 2.0 ** -24 * np.abs(x64 @ w64.T) + (nb + 20) * 2.0 ** -149
+    err = np.abs(g64 - x64 @ w64.T)
+    assert (err <= tol)[fits].all(), float(np.max((err / tol)[fits]))
+    again = fp4.fp4_rows_product(x, w, out_dtype=torch.float32)
+    assert torch.equal(again.view(torch.int32), got.view(torch.int32))
+
+
+def test_rows_product_mx_tiny_rows_and_large_scales(fp4):
+    """A row of 2^-60 against scales of 2^115 to 2^125 over a long k, and the
+    same with a zero block of the largest scale beside blocks of the least."""
+    r = np.random.default_rng(8)
+    codes = r.integers(0, 16, (64, 8192))
+    w, w64 = matrix(fp4, codes, r.integers(242, 253, (64, 256)), "mx")
+    x, x64 = bf16(r.standard_normal((2, 8192)) * 2.0 ** -60)
+    check_rows(fp4.fp4_rows_product(x, w, out_dtype=torch.float32), x64, w64, torch.float32)
+    byte = np.zeros((64, 256), dtype=np.int64)
+    byte[:, ::7] = 254
+    codes.reshape(64, 256, 32)[:, ::7] = 0
+    w, w64 = matrix(fp4, codes, byte, "mx")
+    x, x64 = bf16(r.standard_normal((2, 8192)) * 2.0 ** 120)
+    check_rows(fp4.fp4_rows_product(x, w, out_dtype=torch.float32), x64, w64, torch.float32)
