@@ -653,7 +653,7 @@ muon_status_t muon_fp4_get_status(void* stream) {
   }
   unsigned v = 0, zero = 0;
   if (cudaMemcpyFromSymbol(&v, g_fp4_status, sizeof(v)) != cudaSuccess ||
-      (v != 0 && cudaMemcpyToSymbol(g_fp4_status, &zero, sizeof(zero)) != cudaSuccess)) {
+      (v != 0 && (cudaMemcpyToSymbol(g_fp4_status, &zero, sizeof(zero)) != cudaSuccess || !uploads_done()))) {
     cudaGetLastError();
     return MUON_ERR_CUDA;
   }

@@ -914,7 +914,7 @@ muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs,
       if (!put(pl->items_d, items.data(), items.size() * sizeof(Item)) ||
           !put(pl->tiles_d, tiles.data(), tiles.size() * sizeof(TileRef)) ||
           !put(pl->deqs_d, deqs.data(), deqs.size() * sizeof(Deq)) ||
-          !put(pl->refs_d, refs.data(), refs.size() * sizeof(DeqRef))) {
+          !put(pl->refs_d, refs.data(), refs.size() * sizeof(DeqRef)) || !uploads_done()) {
         cudaGetLastError();
         cudaFree(pl->dmem);
         delete pl;

@@ -110,6 +110,12 @@ inline bool any_overlap(std::vector<ByteRange>& v) {
   return false;
 }
 
+// Host: wait until the synchronous calls' copies and memsets so far are on the
+// device.  A copy from pageable memory returns once its source has been read,
+// a memset at once, and non-blocking streams do not wait for the stream of
+// these calls, so a plan's tables are waited for before it is handed out.
+inline bool uploads_done() { return cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess; }
+
 // Tile of the fp32 path's GEMM phases: .x matrix, .y row0, .z col0, .w unused.
 using TileDesc = int4;
 
