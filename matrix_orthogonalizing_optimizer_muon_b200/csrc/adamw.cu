@@ -211,6 +211,7 @@ extern "C" muon_status_t muon_adamw_init(muon_adamw_plan_t* out, const muon_adam
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   bool ok = cudaMemcpy(pl->chunks_d, chunks.data(), chunks.size() * sizeof(AdamChunk), cudaMemcpyHostToDevice) ==
             cudaSuccess;
+  ok = ok && uploads_done();
   ok = ok && cudaHostAlloc(reinterpret_cast<void**>(&pl->pinned), n * sizeof(AdamPtrs), cudaHostAllocDefault) ==
                  cudaSuccess;
   ok = ok && cudaEventCreateWithFlags(&pl->ev, cudaEventDisableTiming) == cudaSuccess;

@@ -814,7 +814,7 @@ extern "C" muon_status_t muon_entropy_init(muon_entropy_plan_t* out, const int64
             cudaMemcpy(pl->tiles_d, tiles.data(), tiles.size() * sizeof(int4), cudaMemcpyHostToDevice) == cudaSuccess &&
             cudaMemcpy(pl->bis_d, bis.data(), bis.size() * sizeof(int2), cudaMemcpyHostToDevice) == cudaSuccess &&
             cudaMemset(pl->ctl.status, 0, sizeof(unsigned)) == cudaSuccess &&
-            cudaMemset(pl->ctl.computed, 0, n * sizeof(int)) == cudaSuccess;
+            cudaMemset(pl->ctl.computed, 0, n * sizeof(int)) == cudaSuccess && uploads_done();
   ok = ok && cudaHostAlloc(reinterpret_cast<void**>(&pl->pinned), n * sizeof(float*), cudaHostAllocDefault) ==
                  cudaSuccess;
   ok = ok && cudaEventCreateWithFlags(&pl->ev, cudaEventDisableTiming) == cudaSuccess;
@@ -963,7 +963,7 @@ extern "C" muon_status_t muon_entropy_get_status(muon_entropy_plan_t pl, int32_t
   }
   unsigned s = 0;
   if (cudaMemcpy(&s, pl->ctl.status, sizeof(unsigned), cudaMemcpyDeviceToHost) != cudaSuccess ||
-      cudaMemset(pl->ctl.status, 0, sizeof(unsigned)) != cudaSuccess ||
+      cudaMemset(pl->ctl.status, 0, sizeof(unsigned)) != cudaSuccess || !uploads_done() ||
       (computed_out != nullptr &&
        cudaMemcpy(computed_out, pl->ctl.computed, pl->n * sizeof(int32_t), cudaMemcpyDeviceToHost) != cudaSuccess)) {
     cudaGetLastError();

@@ -863,6 +863,7 @@ muon_status_t muon_init_ex(muon_plan_t* out, const muon_param_t* params, int32_t
   ok = ok && cudaMemset(ws.norm_count, 0, n * sizeof(unsigned)) == cudaSuccess;
   ok = ok && cudaMemset(ws.status, 0, sizeof(unsigned)) == cudaSuccess;
   ok = ok && cudaMemset(ws.s, 0, n * sizeof(float)) == cudaSuccess;
+  ok = ok && uploads_done();
   for (auto& sl : pl->slots) {
     ok = ok && cudaHostAlloc(reinterpret_cast<void**>(&sl.pinned), n * sizeof(MatPtrs), cudaHostAllocDefault) ==
                    cudaSuccess;
@@ -992,7 +993,7 @@ muon_status_t muon_get_status(muon_plan_t pl) {
   if (cudaStreamSynchronize(pl->last_stream) != cudaSuccess) return MUON_ERR_CUDA;
   unsigned v = 0;
   if (cudaMemcpy(&v, pl->ws.status, sizeof(unsigned), cudaMemcpyDeviceToHost) != cudaSuccess) return MUON_ERR_CUDA;
-  if (v != 0 && cudaMemset(pl->ws.status, 0, sizeof(unsigned)) != cudaSuccess) return MUON_ERR_CUDA;
+  if (v != 0 && (cudaMemset(pl->ws.status, 0, sizeof(unsigned)) != cudaSuccess || !uploads_done())) return MUON_ERR_CUDA;
   if (v & kStatusTimeout) return MUON_ERR_TIMEOUT;
   if (v & kStatusNonFinite) return MUON_ERR_NONFINITE;
   return MUON_OK;

@@ -168,6 +168,7 @@ muon_status_t muon_pack_init(muon_pack_plan_t* out, const muon_segment_t* segs, 
   bool ok = cudaMemcpy(pl->segs_d, host.data(), n * sizeof(SegDev), cudaMemcpyHostToDevice) == cudaSuccess;
   ok = ok && cudaMemcpy(pl->chunks_d, chunks.data(), chunks.size() * sizeof(ChunkRef), cudaMemcpyHostToDevice) ==
                  cudaSuccess;
+  ok = ok && muon::uploads_done();
   if (!ok) {
     cudaGetLastError();
     cudaFree(pl->dmem);
