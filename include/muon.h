@@ -506,8 +506,8 @@ MUON_API muon_status_t muon_fp4_dequantize(const muon_fp4_matrix_t* m, void* dst
  * the same forms for all) in one pass, whatever their count: the 4-bit copies
  * of a model's weights after an optimizer step.  The pointers are kept; the
  * caller keeps the buffers alive.  values_dtype >= 0: muon_fp4_values also
- * writes every form's values, to values_cols / values_rows.  Uploads its
- * tables with synchronous copies.  Errors: as muon_fp4_quantize, NO_MEMORY.
+ * writes every form's values, to values_cols / values_rows.  Quantises nothing
+ * yet.  Its tables are on the device when it returns.  Errors: as muon_fp4_quantize, NO_MEMORY.
  * On error *out is NULL. */
 typedef struct muon_fp4_plan_s* muon_fp4_plan_t;
 MUON_API muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs, int32_t n,

@@ -11,9 +11,10 @@ the rounding and the storage.
     y = fp4_product(q, wq)                   # q @ wq.T, 4-bit tensor-core products
     y = fp4_rows_product(tokens, wq)         # a few bf16 rows, unquantised
 
-The weights' 4-bit copies are refreshed after an optimizer step by one plan:
+The weights' 4-bit copies are made, and refreshed after an optimizer step, by
+one plan:
 
-    plan = Fp4Plan(weights, along="both")
+    plan = Fp4Plan(weights, along="both")    # quantises them as they are now
     opt = HybridStep(..., fp4=plan)          # or plan.run() after any step
     y, kept = fp4_linear(x, plan.matrices[i])
     dx, dw = fp4_linear_backward(kept, dy)   # dw is the gradient that the step takes
@@ -22,7 +23,8 @@ Work is enqueued on `stream`, or the current stream of the operands' device;
 tensors that a call allocates belong to that stream.  An operand made on
 another stream has to be ready before, as for any torch call, and must not be
 freed there before the call's work is done (torch's record_stream).  Nothing
-here builds an autograd graph or synchronises.
+here builds an autograd graph, and nothing but a plan's set-up and the status
+read synchronises.
 """
 
 from __future__ import annotations
@@ -243,9 +245,10 @@ def fp4_quantize(x: torch.Tensor, *, fmt: str = "nv", along: str = "cols", out=N
 class Fp4Plan:
     """Quantises a fixed list of tensors [R, C] (one dtype) in one pass each
     run: the 4-bit copies of a model's weights.  `matrices[i]` is the
-    Fp4Matrix of tensors[i], or the pair (cols, rows) for along="both".  With
-    `values` (bf16 or fp32) the plan also holds dense tensors for
-    ``dequantize``."""
+    Fp4Matrix of tensors[i], or the pair (cols, rows) for along="both"; the
+    set-up runs the plan once, so they hold the tensors as they are then, and
+    waits for that.  With `values` (bf16 or fp32) the plan also holds dense
+    tensors for ``dequantize``."""
 
     def __init__(self, tensors, *, fmt: str = "nv", along: str = "cols", values: torch.dtype | None = None, stream=None):
         tensors = list(tensors)
@@ -275,6 +278,8 @@ class Fp4Plan:
                 srcs[i] = src
             self._plan = L.muon_fp4_init(srcs, len(tensors), -1 if values is None else _GDT[values],
                                          _current(self.device))
+            L.muon_fp4_run(self._plan, _current(self.device))
+            torch.cuda.current_stream(self.device).synchronize()  # a next run, on any stream, must not overlap
 
     def run(self, stream=None) -> None:
         """Quantise every tensor as it is now."""

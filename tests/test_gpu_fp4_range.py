@@ -138,3 +138,20 @@ def test_rows_product_mx_tiny_rows_and_large_scales(fp4):
     w, w64 = matrix(fp4, codes, byte, "mx")
     x, x64 = bf16(r.standard_normal((2, 8192)) * 2.0 ** 120)
     check_rows(fp4.fp4_rows_product(x, w, out_dtype=torch.float32), x64, w64, torch.float32)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_a_new_plan_holds_its_tensors(fp4, fmt):
+    """The documented order, a layer on a plan that was only made: the bits of the weights' own quantisation."""
+    junk = torch.full((1 << 24,), 0x77, dtype=torch.uint8, device="cuda")
+    del junk  # what the plan's storage may hold before
+    r = np.random.default_rng(3)
+    ws = [torch.from_numpy(r.standard_normal(s).astype(np.float32)).cuda() for s in ((300, 200), (64, 96))]
+    x = torch.from_numpy(r.standard_normal((40, 300)).astype(np.float32)).cuda()
+    plan = fp4.Fp4Plan(ws, fmt=fmt, along="both", values=torch.bfloat16)
+    y, _ = fp4.fp4_linear(x, plan.matrices[0])
+    assert torch.equal(y, fp4.fp4_linear(x, ws[0], fmt=fmt)[0])
+    for i, w in enumerate(ws):
+        for m, q in zip(plan.matrices[i], fp4.fp4_quantize(w, fmt=fmt, along="both")):
+            assert torch.equal(m.data, q.data) and torch.equal(m.scales, q.scales)
+    plan.close()
