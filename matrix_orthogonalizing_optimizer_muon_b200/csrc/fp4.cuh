@@ -182,11 +182,11 @@ __host__ __device__ __forceinline__ int tensor_exponent(uint32_t amax_bits) {
 
 // Scale of one block from the bits of its largest magnitude (anything at or
 // above the bits of infinity says that the block holds a NaN or an infinity;
-// the codes of such a block do not matter).
+// the codes of such a block do not matter, but for those past k).
 struct BlockScale {
   uint32_t byte;       // the scale byte
   uint64_t r, r_rest;  // the scale's reciprocal as a pair of equal floats: MX r alone, exact; NV rounded down,
-                       // and what is left of it (both 0 for a zero scale)
+                       // and what is left of it (both 0 for a zero scale and a NaN, so that the zeros past k are code 0)
 };
 
 // A matrix's scale and what its blocks' scales are found with.
@@ -231,8 +231,9 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, const Matr
     const float a = rcp_approx(d);
     const float r = __fmaf_rd(fmaf(-d, a, 1.0f), a, a);
     const float rest = fmaf(-d, r, 1.0f) * r;
-    b.r = b.byte != 0u ? twice(r) : 0u;
-    b.r_rest = b.byte != 0u ? twice(rest) : 0u;
+    const bool some = b.byte != 0u && b.byte != 0x7Fu;
+    b.r = some ? twice(r) : 0u;
+    b.r_rest = some ? twice(rest) : 0u;
   } else {
     const int e = static_cast<int>(amax_bits >> 23) - 2;
     b.byte = e < 0 ? 0u : static_cast<uint32_t>(e);

@@ -155,3 +155,18 @@ def test_a_new_plan_holds_its_tensors(fp4, fmt):
         for m, q in zip(plan.matrices[i], fp4.fp4_quantize(w, fmt=fmt, along="both")):
             assert torch.equal(m.data, q.data) and torch.equal(m.scales, q.scales)
     plan.close()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_codes_past_k_are_zero_beside_a_value_that_is_not_finite(fp4, bad, dtype, fmt):
+    """The last, partial block of a row and of a column holds a NaN or an infinity; the storage past it is 0."""
+    for rows, k in ((150, 200), (3, 17), (70, 33), (1, 1)):
+        x = torch.randn(rows, k, device="cuda").to(dtype)
+        x[rows - 1, k - 1] = bad
+        for m in fp4.fp4_quantize(x, fmt=fmt, along="both"):
+            data = m.data.view(m.rows, -1)
+            codes = torch.stack([data & 15, data >> 4], -1).flatten(1)
+            assert codes.shape[1] >= m.k and (codes[:, m.k:] == 0).all()
+            assert torch.isnan(m.dequantize()[-1, -1])
