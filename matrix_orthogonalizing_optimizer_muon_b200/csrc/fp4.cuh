@@ -173,8 +173,7 @@ __device__ __forceinline__ void e2m1_values8(uint32_t w, float s, float* v) {
 // The matrix's power of two: the least g = 2^e, e >= -100, with amax <= 2688 g,
 // so that the largest block scale amax / (6 g) is at most 448, e4m3's largest.
 // 2688 = 1.3125 * 2^11, so e follows from the bits of amax (a finite fp32).
-// The floor keeps every scale, its reciprocal and the remainders of the
-// division below normal.
+// The floor keeps the least scales, their quotients and remainders below normal.
 __host__ __device__ __forceinline__ int tensor_exponent(uint32_t amax_bits) {
   const int e = static_cast<int>(amax_bits >> 23) - 127 - 11 + ((amax_bits & 0x7FFFFFu) > 0x280000u ? 1 : 0);
   return e < -100 ? -100 : e;
@@ -219,14 +218,15 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, const Matr
   BlockScale b;
   if (kNv) {
     // amax / (6 g), the product with the reciprocal corrected once by its
-    // remainder, is rounded twice, to fp32 and then to e4m3, with the result
+    // remainder (Markstein's division), is rounded twice, to fp32 and then to e4m3, with the result
     // of one rounding: a quotient by 6 g (significand 1.5) that is not itself
     // a midpoint of e4m3 (5 significant bits) lies more than half an fp32
     // step from every midpoint.
     const float x = __uint_as_float(amax_bits), q = x * m.sixth;
     b.byte = __nv_cvt_float_to_fp8(fmaf(-fmaf(q, m.six, -x), m.sixth, q), __NV_SATFINITE, __NV_E4M3);
     if (amax_bits >= 0x7F800000u) b.byte = 0x7Fu;
-    // 1 / d as r + rest, r rounded down so that neither is negative
+    // 1 / d as r + rest, r rounded down so that neither is negative: one
+    // Newton-Raphson step on the approximate reciprocal, and its remainder
     const float d = e4m3_value(b.byte) * m.g;  // exact: four significant bits; below 2^126
     const float a = rcp_approx(d);
     const float r = __fmaf_rd(fmaf(-d, a, 1.0f), a, a);
@@ -249,8 +249,13 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, const Matr
 // 2^-46 of it, which is exact where the quotient has few bits and else on the
 // right side of every border: a quotient by a four-bit scale that is no
 // midpoint of e2m1 (three significant bits) is more than half an fp32 step
-// from every midpoint.  A zero keeps its sign, since r and rest are not
-// negative.  Both lanes in one instruction each (f32x2).
+// from every midpoint.  From scales of about 2^102 on `rest` is subnormal and
+// the pair is good to fewer bits, 2^-25 at 2^125; the codes are still right at
+// every midpoint and both its neighbours, by exact arithmetic over all scale
+// bytes and the highest g, but for the scale 448 under g = 2^117, and there
+// the largest finite amax is 342 times 6 g, a scale of 352 at most.  A zero
+// keeps its sign, since r and rest are not negative.  Both lanes in one
+// instruction each (f32x2).
 template <bool kNv>
 __device__ __forceinline__ uint64_t quotients(float x0, float x1, const BlockScale& b) {
   uint64_t x, q;

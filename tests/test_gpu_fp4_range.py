@@ -170,3 +170,35 @@ def test_codes_past_k_are_zero_beside_a_value_that_is_not_finite(fp4, bad, dtype
             codes = torch.stack([data & 15, data >> 4], -1).flatten(1)
             assert codes.shape[1] >= m.k and (codes[:, m.k:] == 0).all()
             assert torch.isnan(m.dequantize()[-1, -1])
+
+
+@pytest.mark.parametrize("rows", [1, 200])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_nv_midpoints_near_the_largest_values(fp4, dtype, rows):
+    """Midpoints of the codes and their fp32 neighbours under every scale of
+    the matrix scales 2^112 to 2^117: bitwise the oracle, as a small matrix and
+    behind a pass of its own."""
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    top = float(np.finfo(np.float32).max)
+    for e in (112, 115, 116, 117):
+        blocks = []
+        for s in o.E4M3[1:]:
+            d = s * 2.0 ** e
+            if 6 * d * (1 + 2.0 ** -4) > top:
+                continue
+            v = (mids * d).astype(np.float32)
+            for near in (v, np.nextafter(v, np.float32(0)), np.nextafter(v, np.float32(np.inf))):
+                row = np.zeros(16, dtype=np.float32)
+                row[0], row[1:8], row[8:15] = 6 * d, near, -near
+                blocks.append(row)
+        x = np.stack(blocks).reshape(1, -1)
+        x[0, 0] = min(2688.0 * 2.0 ** e, top)  # the matrix's largest: g = 2^e
+        t = torch.from_numpy(np.repeat(x, rows, 0)).cuda().to(dtype)
+        m64 = t.double().cpu().numpy()
+        want = o.quantize(m64, "nv")
+        assert want.g == 2.0 ** e
+        got = fp4.fp4_quantize(t, fmt="nv")
+        data, scales = want.stored()
+        fine = np.repeat(want.scale_bytes != 127, 8, axis=1)  # as bf16 the largest fp32 is an infinity: its block has no codes
+        assert np.array_equal(got.data.cpu().numpy().reshape(data.shape)[:, :fine.shape[1]][fine], data[:, :fine.shape[1]][fine])
+        assert np.array_equal(got.scales.cpu().numpy(), scales)
