@@ -146,6 +146,17 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
   return __half2float(__half(h));
 }
 
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// v as m 2^e with 1 <= |m| < 2, subnormals too (v itself and e = 0 for zeros and what is not finite).
+__device__ __forceinline__ float significand(float v, int& e) {
+  const bool below = fabsf(v) < pow2(-126), plain = v == 0.0f || !(fabsf(v) < __uint_as_float(0x7F800000u));
+  const uint32_t b = __float_as_uint(below ? v * pow2(64) : v);
+  e = plain ? 0 : static_cast<int>((b >> 23) & 255u) - (below ? 127 + 64 : 127);
+  return plain ? v : __uint_as_float((b & 0x807FFFFFu) | 0x3F800000u);
+}
+
 // Eight codes (lowest four bits first) as four fp16 pairs.
 __device__ __forceinline__ void e2m1_expand8(uint32_t w, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"

@@ -355,9 +355,19 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const int quad = warp & 3, half = (warp - kEpi0) >> 2;
     constexpr int kPer = kBn / 2 / 32;  // 32-column blocks of a warp
     const uint32_t tempty = kCg == 2 ? map_to_rank(tempty_bar, 0) : tempty_bar;
-    // the smaller scale first: nothing passes fp32's range that the result does not pass
-    const float sa = kNv ? *g.ga : 1.0f, sb = kNv ? *g.gb : 1.0f;
-    const float ga = fabsf(sa) < fabsf(sb) ? sa : sb, gb = fabsf(sa) < fabsf(sb) ? sb : sa;
+    // g_A g_B as two factors, half of its exponent in each: both shrink or both
+    // grow, so that nothing passes either end of fp32's range that the result
+    // does not pass.  (Below 2^-252 a sum gives 0.)
+    float ga = 1.0f, gb = 1.0f;
+    if (kNv) {
+      const float sa = *g.ga, sb = *g.gb;
+      int ea, eb;
+      ga = significand(fabsf(sa) < fabsf(sb) ? sa : sb, ea);
+      gb = significand(fabsf(sa) < fabsf(sb) ? sb : sa, eb);
+      const int e = max(ea + eb, -252);
+      ga *= pow2(e >> 1);
+      gb *= pow2(e - (e >> 1));
+    }
     const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * (kBn / 2);
     uint8_t* stg = smem + C::kEpi + (warp - kEpi0) * kStagingBytes;
     int turn = 0;

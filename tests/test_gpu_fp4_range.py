@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import oracle.fp4_oracle as o
-from test_gpu_fp4 import check_rows
+from test_gpu_fp4 import check_product, check_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -49,7 +49,7 @@ def test_rows_product_keeps_a_value_far_below_the_largest(fp4, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
-@pytest.mark.parametrize("t,n,k", [(1, 40, 96), (3, 300, 2048), (7, 33, 1409), (12, 100, 512), (32, 70, 200), (5, 48, 10500)])
+@pytest.mark.parametrize("t,n,k", [(1, 40, 96), (3, 300, 2048), (7, 33, 1409), (12, 100, 512), (32, 70, 200), (5, 48, 10500), (20, 50, 6000)])
 def test_rows_product_of_rows_that_spread_over_the_whole_range(fp4, t, n, k, fmt):
     """Every row's values lie in groups down to 2^-250 of its largest, and each
     row of W is zero under all groups above one of its own: each output within
@@ -202,3 +202,22 @@ def test_quantize_nv_midpoints_near_the_largest_values(fp4, dtype, rows):
         fine = np.repeat(want.scale_bytes != 127, 8, axis=1)  # as bf16 the largest fp32 is an infinity: its block has no codes
         assert np.array_equal(got.data.cpu().numpy().reshape(data.shape)[:, :fine.shape[1]][fine], data[:, :fine.shape[1]][fine])
         assert np.array_equal(got.scales.cpu().numpy(), scales)
+
+
+@pytest.mark.parametrize("ga,gb", [(1.37 * 2.0 ** -140, 1.7 * 2.0 ** 122), (2.0 ** 120, -(2.0 ** -149)),
+                                   (1.9 * 2.0 ** -120, 1.1 * 2.0 ** 60), (2.0 ** -100, 2.0 ** -20), (2.0 ** 127, 2.0 ** -127)])
+@pytest.mark.parametrize("m", [40, 2500])
+def test_products_with_tensor_scales_at_the_ends_of_fp32(fp4, m, ga, gb):
+    """Tensor scales of a checkpoint, subnormal ones too: fp32 sums times both
+    scales, and rows of X as large or small as the scale is small or large."""
+    r = np.random.default_rng(9)
+    n, k = 1300, 200
+    both = []
+    for rows, g in ((m, ga), (n, gb)):
+        g = float(np.float32(g))
+        both.append(matrix(fp4, r.integers(0, 16, (rows, k)), r.integers(1, 127, (rows, -(-k // 16))), "nv", g))
+    (a, a64), (b, b64) = both
+    check_product(fp4.fp4_product(a, b, out_dtype=torch.float32), a64, b64, torch.float32)
+    up = float(np.clip(-np.round(np.log2(abs(gb))), -105, 105))
+    x, x64 = bf16(r.standard_normal((5, k)) * 2.0 ** up)
+    check_rows(fp4.fp4_rows_product(x, b, out_dtype=torch.float32), x64, b64, torch.float32)
