@@ -555,6 +555,15 @@ MUON_API muon_status_t muon_fp4_rows_product(const void* x, int64_t t, int64_t l
  * stream that is being captured.  CUDA errors: MUON_ERR_CUDA. */
 MUON_API muon_status_t muon_fp4_get_status(void* stream);
 
+/* Failure-detection test hook (host-side injection; nothing faults).  The next
+ * muon_fp4_product launch of the calling host thread makes one thread of every
+ * CTA wait on a barrier that nothing arrives at, for at most wait_ns
+ * nanoseconds (1 .. 10^9), before any load or tensor-core instruction is
+ * issued.  The wait runs out, the launch does no work (its output stays as it
+ * was), and muon_fp4_get_status reports MUON_ERR_TIMEOUT; later calls run
+ * normally.  Errors: INVALID_ARG (wait_ns out of range). */
+MUON_API muon_status_t muon_fp4_inject_wait_timeout(uint32_t wait_ns);
+
 #ifdef __cplusplus
 }
 #endif

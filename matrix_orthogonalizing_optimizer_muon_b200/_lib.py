@@ -48,7 +48,7 @@ EXPORTED = ("muon_hparams_default", "muon_init", "muon_init_ex", "muon_num_waves
             "muon_entropy_get_status", "muon_entropy_profile", "muon_entropy_destroy", "muon_pack_init",
             "muon_pack_run", "muon_pack_destroy", "muon_fp4_sizes", "muon_fp4_quantize", "muon_fp4_dequantize",
             "muon_fp4_init", "muon_fp4_run", "muon_fp4_values", "muon_fp4_destroy", "muon_fp4_product",
-            "muon_fp4_rows_product", "muon_fp4_get_status")
+            "muon_fp4_rows_product", "muon_fp4_get_status", "muon_fp4_inject_wait_timeout")
 
 
 class muon_param_t(ctypes.Structure):
@@ -196,6 +196,8 @@ def load() -> ctypes.CDLL:
     lib.muon_fp4_rows_product.restype = ctypes.c_int
     lib.muon_fp4_get_status.argtypes = [P]
     lib.muon_fp4_get_status.restype = ctypes.c_int
+    lib.muon_fp4_inject_wait_timeout.argtypes = [ctypes.c_uint32]
+    lib.muon_fp4_inject_wait_timeout.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -405,3 +407,7 @@ def muon_fp4_rows_product(x_ptr: int, t: int, ldx: int, w: muon_fp4_matrix_t, ou
 
 def muon_fp4_get_status(stream: int) -> int:
     return int(load().muon_fp4_get_status(ctypes.c_void_p(stream)))
+
+
+def muon_fp4_inject_wait_timeout(wait_ns: int) -> None:
+    check(load().muon_fp4_inject_wait_timeout(int(wait_ns)), "muon_fp4_inject_wait_timeout")

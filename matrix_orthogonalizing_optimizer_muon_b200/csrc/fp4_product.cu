@@ -77,6 +77,7 @@ struct ProdArgs {
   const float* gb;
   int32_t m, n, nk, tiles_m, tiles_n;
   int32_t out_dtype, accumulate, vec;
+  uint32_t test_wait_ns;  // 0; > 0 only for the failure-detection test (muon_fp4_inject_wait_timeout)
 };
 
 template <int kCg>
@@ -241,7 +242,17 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   pdl_wait();
   pdl_trigger();
 
-  if (warp == 0) {
+  if (g.test_wait_ns != 0) {
+    // Failure-detection test: one thread per CTA waits, with the short limit, on
+    // a barrier on which nothing arrives before the last MMA, and gives up.  No
+    // role starts, so no load or tensor-core instruction is ever issued.
+    if (threadIdx.x == 0 && !wait_bounded_ns(drain_bar, 0u, nullptr, g.test_wait_ns)) give_up(abort_flag);
+    __syncthreads();
+  }
+
+  if (g.test_wait_ns != 0 && *abort_flag != 0) {
+    // nothing
+  } else if (warp == 0) {
     // ------------------------------------------------------------ producer
     const void* map = lane == 0 ? &map_a : lane == 1 ? &map_b : lane == 2 ? &map_sa : &map_sb;
     if (lane < 4) prefetch_tensormap(map);
@@ -514,6 +525,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 }
 
 // ---------------------------------------------------------------- host
+thread_local uint32_t t_test_wait_ns = 0;  // for this thread's next launch
+
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -646,6 +659,8 @@ muon_status_t muon_fp4_product(const muon_fp4_matrix_t* a, const muon_fp4_matrix
   const int64_t pitch = a->rows == 1 ? (b->rows + 7) / 8 * 8 : ldo;
   g.vec = (o % 16 == 0 && pitch * es % 16 == 0 && pitch * es < (int64_t(1) << 40)) ? 1 : 0;
   if (g.vec) g.ldo = pitch;
+  g.test_wait_ns = t_test_wait_ns;
+  t_test_wait_ns = 0;
   const bool nv = a->format == MUON_FP4_NV;
   // pairs where there are enough 256 x 256 tiles for them, single CTAs below
   const int64_t pair_tiles = ((a->rows + 255) / 256) * ((b->rows + 255) / 256);
@@ -654,6 +669,12 @@ muon_status_t muon_fp4_product(const muon_fp4_matrix_t* a, const muon_fp4_matrix
               : launch_product<2, 256, false>(*a, *b, g, dev, sms, st);
   return nv ? launch_product<1, 128, true>(*a, *b, g, dev, sms, st)
             : launch_product<1, 128, false>(*a, *b, g, dev, sms, st);
+}
+
+muon_status_t muon_fp4_inject_wait_timeout(uint32_t wait_ns) {
+  if (wait_ns < 1 || wait_ns > 1000000000u) return MUON_ERR_INVALID_ARG;
+  t_test_wait_ns = wait_ns;
+  return MUON_OK;
 }
 
 muon_status_t muon_fp4_get_status(void* stream) {
