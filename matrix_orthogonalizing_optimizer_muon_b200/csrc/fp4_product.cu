@@ -55,7 +55,7 @@ struct Cfg {
   static constexpr int kSaBytes = kAtoms * kAtomBytes;
   static constexpr int kSbBytes = kAtoms * kAtomBytes * (kBn / 128);  // every CTA needs the scales of all kBn columns
   static constexpr int kStage = kABytes + kBBytes + kSaBytes + kSbBytes;
-  static constexpr int kStages = kBn == 256 ? 5 : 5;
+  static constexpr int kStages = 5;
   static constexpr int kEpi = kStages * kStage;
   static constexpr int kBar = kEpi + kEpiWarpsP * kStagingBytes;
   static constexpr int kMisc = kBar + (2 * kStages + 3) * 8;
@@ -239,8 +239,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   if (kCg == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();
-  pdl_trigger();
 
   if (g.test_wait_ns != 0) {
     // Failure-detection test: one thread per CTA waits, with the short limit, on

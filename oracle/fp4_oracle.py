@@ -107,11 +107,6 @@ def product(a: Fp4, b: Fp4) -> np.ndarray:
     return a.values() @ b.values().T
 
 
-def product_bound(a: np.ndarray, b: np.ndarray) -> np.ndarray:
-    """Sum of the products' magnitudes, per output: what errors of the sums scale with."""
-    return np.abs(a) @ np.abs(b).T
-
-
 def linear(x, w, dy, fmt):
     """(y, dx, dw) of a linear layer whose three products round their
     operands to 4 bits along the summed dimension; w is [K, N]."""
