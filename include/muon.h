@@ -493,7 +493,8 @@ MUON_API muon_status_t muon_fp4_sizes(int32_t format, int64_t rows, int64_t k, i
  * format.  An empty source is a no-op.  No output may overlap the source or
  * another output.  Deterministic: every output bit is fixed by the source.
  * Errors: INVALID_ARG, SHAPE_MISMATCH (a form's shape is not the source's),
- * ALIAS, UNSUPPORTED (2^31 tiles of 128 x 128 or more), CUDA. */
+ * ALIAS, UNSUPPORTED (2^31 tiles of 64 rows x 128 columns or more, the rows
+ * rounded up to 128), CUDA. */
 MUON_API muon_status_t muon_fp4_quantize(const muon_fp4_source_t* src, void* stream);
 
 /* dst [rows, k] (row pitch ld elements, dst_dtype) = the values of a 4-bit
@@ -507,8 +508,8 @@ MUON_API muon_status_t muon_fp4_dequantize(const muon_fp4_matrix_t* m, void* dst
  * of a model's weights after an optimizer step.  The pointers are kept; the
  * caller keeps the buffers alive.  values_dtype >= 0: muon_fp4_values also
  * writes every form's values, to values_cols / values_rows.  Quantises nothing
- * yet.  Its tables are on the device when it returns.  Errors: as muon_fp4_quantize, NO_MEMORY.
- * On error *out is NULL. */
+ * yet.  Its tables are on the device when it returns.  Errors: as
+ * muon_fp4_quantize, NO_MEMORY.  On error *out is NULL. */
 typedef struct muon_fp4_plan_s* muon_fp4_plan_t;
 MUON_API muon_status_t muon_fp4_init(muon_fp4_plan_t* out, const muon_fp4_source_t* srcs, int32_t n,
                                      int32_t values_dtype, void* stream);
@@ -543,8 +544,10 @@ MUON_API muon_status_t muon_fp4_product(const muon_fp4_matrix_t* a, const muon_f
 /* out [t, w.rows] (row pitch ldo elements, out_dtype) = X W^T for a few rows X
  * [t, w.k] in bf16 (row pitch ldx elements), 0 <= t <= MUON_FP4_MAX_ROWS, and
  * a 4-bit matrix W, asynchronously on `stream`: the form for single tokens,
- * in which X keeps its precision and a row's result does not depend on the
- * other rows.  fp32 sums.  Errors: INVALID_ARG, ALIAS, CUDA. */
+ * in which X is taken exactly (rows that spread over more than 32 exponents in
+ * several passes over W, 8 at most), MX scales and g over their whole range,
+ * and a row's result does not depend on the other rows.  fp32 sums.  Errors:
+ * INVALID_ARG, ALIAS, UNSUPPORTED (not an sm_100 device), CUDA. */
 #define MUON_FP4_MAX_ROWS 32
 MUON_API muon_status_t muon_fp4_rows_product(const void* x, int64_t t, int64_t ldx, const muon_fp4_matrix_t* w,
                                              void* out, int64_t ldo, int32_t out_dtype, void* stream);

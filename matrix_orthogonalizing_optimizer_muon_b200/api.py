@@ -301,8 +301,10 @@ class HybridStep:
     learning rate and one weight decay for both; the RMSNorm gains keep their
     weight decay (Appendix D, "Training stability").  Both plans enqueue on
     the same stream, Muon first; nothing waits on the host.  With `fp4` (an
-    ``fp4.Fp4Plan`` over the updated weights) every step ends by quantising
-    them to the 4-bit copies that the next forward and backward passes read.
+    ``fp4.Fp4Plan`` over the updated weights; that it holds these very tensors
+    is the caller's to see to) every step ends by quantising them to the 4-bit
+    copies that the next forward and backward passes read.  ``status`` is the
+    Muon plan's; the products report by ``fp4.fp4_status``.
 
         opt = HybridStep([W.shape for W in mats], [p.numel() for p in vecs],
                          momenta=Ms, adam_states=[(m, v), ...])

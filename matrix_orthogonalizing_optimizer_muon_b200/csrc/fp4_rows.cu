@@ -9,9 +9,9 @@
 // operands, and needs both in shared memory.)
 //
 //   W  goes to shared memory by cp.async, in steps of 128 k of a warp's 16
-//      rows, kDepth - 1 steps ahead (plain loads into registers were moved
-//      down to their use by the compiler: 36 us instead of 25 for
-//      65536 x 2048).  A code becomes an fp16 by one conversion for two.
+//      rows, kDepth - 1 steps ahead (with plain loads into registers, which
+//      the compiler moved down to their use, 65536 x 2048 had taken 36 us where
+//      the first such ring took 25).  A code becomes an fp16 by one conversion for two.
 //      NV: times the block's scale, exactly (e2m1 x e4m3 has at most six
 //      significant bits within fp16's range).  MX: the exponent of a scale may
 //      be outside fp16's range, so the products of a block are summed from
@@ -792,8 +792,11 @@ cudaError_t launch_rows_w(const RowsArgs& g, int dev, int ctas, int smem, cudaSt
 // copies of X are small and whose barriers overlap (65536 x 2048, NV, t = 1:
 // 19.6 us against 20.3 us as one CTA; 2048 x 8192 7.2 against 8.6 us), more
 // rows as one CTA, which copies X once (t = 16: 26.6 against 27.7 us, t = 32:
-// 39.8 against 46.1 us); eight warps where X takes the shared memory.  (24
-// warps of 80 registers spill: t = 16 39.9 us.)
+// 39.8 against 46.1 us); eight warps where X takes the shared memory.  (These
+// were measured before rows could be taken in parts, which added 2 to 5% to
+// each; now 20.7, 7.1, 26.8, 41.4 us.)  Kernels for more than 16 rows spill 40
+// (NV) or 60 (MX) bytes, MX ones for fewer up to 12; with 24 warps of 80
+// registers the spills took t = 16 to 39.9 us.
 template <bool kNv, int kNg>
 cudaError_t launch_rows(const RowsArgs& g, int dev, int sms, cudaStream_t st) {
   auto smem = [&](int warps) {

@@ -378,7 +378,12 @@ def fp4_linear(x: torch.Tensor, w, *, fmt: str | None = None, out_dtype=torch.bf
     """y = Q(x) Q(w) for x [T, K] and a weight w [K, N], Q the rounding to 4
     bits in blocks along the summed dimension.  w is a tensor, or the pair
     (along cols, along rows) that fp4_quantize or an Fp4Plan made of it with
-    along="both".  Returns (y [T, N], what fp4_linear_backward needs)."""
+    along="both".  Returns (y [T, N], what fp4_linear_backward needs).
+
+    x and w are taken as values: no autograd graph is built, whether they
+    require gradients or not (fp4_linear_backward gives them).  What is kept
+    refers to a given pair itself, so the backward pass belongs before the
+    plan of that pair runs again."""
     _matrix_arg(x, "x")
     device = x.device
     if isinstance(w, torch.Tensor):
