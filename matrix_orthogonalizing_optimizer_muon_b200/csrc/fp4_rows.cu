@@ -219,7 +219,9 @@ __device__ __forceinline__ void stage_part(const RowsArgs& g, int k0, int part, 
     // infinity is in the first (no magnitude is at or above a NaN), a NaN in all
     const float f = pow2(-exponent_of(amax[r], part));
     const int top = field_of(amax[r]) - kWindow * part, bottom = top - kWindow + 1;
-    const float above = part == 0 ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(static_cast<uint32_t>(max(top + 1, 0)) << 23);
+    const float above = part == 0 ? __uint_as_float(0x7FFFFFFFu)
+                        : top > 0 ? __uint_as_float(static_cast<uint32_t>(top + 1) << 23)
+                                  : 0.0f;  // the row has no such part
     const float from = bottom > 1 ? __uint_as_float(static_cast<uint32_t>(bottom) << 23) : 0.0f;
     auto in_part = [&](uint32_t v) {
       const float x = __uint_as_float(v);

@@ -221,3 +221,18 @@ def test_products_with_tensor_scales_at_the_ends_of_fp32(fp4, m, ga, gb):
     up = float(np.clip(-np.round(np.log2(abs(gb))), -105, 105))
     x, x64 = bf16(r.standard_normal((5, k)) * 2.0 ** up)
     check_rows(fp4.fp4_rows_product(x, b, out_dtype=torch.float32), x64, b64, torch.float32)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_rows_product_counts_subnormals_once(fp4, fmt):
+    """Rows whose parts end at the subnormals beside a row with more parts,
+    for every exponent of the largest value: a subnormal is in one part."""
+    w, w64 = matrix(fp4, np.array([[0, 2, 2, 2]]), ones(1, 4, fmt), fmt)
+    for e0 in range(-126, 128, 31):
+        x = np.zeros((32, 4))
+        for i in range(31):
+            x[i] = 2.0 ** min(e0 + i, 127), 3 * 2.0 ** -133, 2.0 ** -126, 2.0 ** -132
+        x[31] = 2.0 ** 127, 2.0 ** -133, 0.0, 0.0
+        x, x64 = bf16(x)
+        got = fp4.fp4_rows_product(x, w, out_dtype=torch.float32).double().cpu().numpy()
+        assert np.array_equal(got, x64 @ w64.T)
