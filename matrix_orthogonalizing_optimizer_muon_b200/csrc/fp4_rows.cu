@@ -156,57 +156,68 @@ __device__ __forceinline__ int x_place(int p) {
   return (kNv ? (p & ~15) + (p & 3) * 4 + ((p >> 2) & 3) : p) * 16;
 }
 
-// Eight values of a row of X with kn of them that starts anywhere; zeros past its end.
-__device__ __forceinline__ void x_piece(const unsigned short* src, int p, int kn, uint32_t (&v)[4]) {
-  if ((reinterpret_cast<uintptr_t>(src) & 15) == 0 && p * 8 + 8 <= kn) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(src) + p);
-    v[0] = q.x;
-    v[1] = q.y;
-    v[2] = q.z;
-    v[3] = q.w;
-    return;
-  }
+// fn(p, the eight values of piece p) for a lane's pieces of a row of X with kn
+// values; zeros past its end.  Four pieces are on their way at a time.
+template <class Fn>
+__device__ __forceinline__ void each_piece(const unsigned short* src, int kn, int pieces, const Fn& fn) {
+  const bool plain = ((reinterpret_cast<uintptr_t>(src) | static_cast<uintptr_t>(2 * kn)) & 15) == 0;
+#pragma unroll 1
+  for (int p = threadIdx.x & 31; p < pieces; p += 128) {
+    uint4 q[4];
+    if (plain) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const unsigned short* e = src + p * 8 + 2 * i;
-    const uint32_t lo = p * 8 + 2 * i < kn ? __ldg(e) : 0u, hi = p * 8 + 2 * i + 1 < kn ? __ldg(e + 1) : 0u;
-    v[i] = lo | (hi << 16);
+      for (int u = 0; u < 4; ++u)
+        q[u] = (p + 32 * u) * 8 < kn ? __ldg(reinterpret_cast<const uint4*>(src) + p + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = (p + 32 * u) * 8 + 2 * i;
+          const uint32_t lo = at < kn ? __ldg(src + at) : 0u, hi = at + 1 < kn ? __ldg(src + at + 1) : 0u;
+          v[i] = lo | (hi << 16);
+        }
+        q[u] = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t v[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+      if (p + 32 * u < pieces) fn(p + 32 * u, v);
+    }
   }
 }
 
-// Stages part `part` of X of [k0, k0 + kc); finds the rows' ranges first when
-// that is the first part.
+// Stages part `part` of X of [k0, k0 + kc); finds the rows' ranges first if
+// they are not known.
 template <bool kNv, int kNg, int kWarps>
-__device__ __forceinline__ void stage_part(const RowsArgs& g, int k0, int part, int t0, int nt, uint8_t* smem,
-                                           uint32_t* amax, int* amin, int* nparts) {
+__device__ __noinline__ void stage_part(const RowsArgs& g, int k0, int part, bool known, int t0, int nt, uint8_t* smem,
+                                           uint32_t* amax, int* nparts) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kn = min(g.kc, g.k - k0);
   const int pieces = (kn + kStepK - 1) / kStepK * (kStepK / 8);
   auto row = [&](int r) {
     return reinterpret_cast<const unsigned short*>(g.x) + static_cast<int64_t>(t0 + r) * g.ldx + k0;
   };
-  if (part == 0) {
+  if (!known) {
     if (threadIdx.x == 0) *nparts = 1;
     __syncthreads();
 #pragma unroll 1
     for (int r = warp; r < nt; r += kWarps) {
       uint32_t a = 0u, least = 0x7FFF7FFFu;
-#pragma unroll 4
-      for (int p = lane; p * 8 < kn; p += 32) {
-        uint32_t v[4];
-        x_piece(row(r), p, kn, v);
+      each_piece(row(r), kn, pieces, [&](int, const uint32_t (&v)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t lo = (v[i] << 16) & 0x7FFF0000u, hi = v[i] & 0x7FFF0000u;
           a = max(a, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
           least = __vmins2(least, wrapped(v[i]));
         }
-      }
+      });
       a = __reduce_max_sync(0xffffffffu, a);
       const int low = __reduce_min_sync(0xffffffffu, least_half(least));
       if (lane == 0) {
         amax[r] = a;
-        amin[r] = low;
         // one part for a row of zeros or without a finite value
         atomicMax(nparts, ((field_of(a) - max(low >> 7, 1)) >> kWindowLog) + 1);
       }
@@ -227,17 +238,15 @@ __device__ __forceinline__ void stage_part(const RowsArgs& g, int k0, int part, 
       const float x = __uint_as_float(v);
       return !(fabsf(x) < from) && !(fabsf(x) >= above) ? x * f : 0.0f;
     };
-#pragma unroll 4
-    for (int p = lane; p < pieces; p += 32) {
-      uint32_t v[4], h[4];
-      x_piece(row(r), p, kn, v);
+    each_piece(row(r), kn, pieces, [&](int p, const uint32_t (&v)[4]) {
+      uint32_t h[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const __half2 c = __floats2half2_rn(in_part(v[i] << 16), in_part(v[i] & 0xFFFF0000u));
         h[i] = *reinterpret_cast<const uint32_t*>(&c);
       }
       *reinterpret_cast<uint4*>(smem + r * g.xpitch + x_place<kNv>(p)) = make_uint4(h[0], h[1], h[2], h[3]);
-    }
+    });
   }
 }
 
@@ -316,15 +325,19 @@ __device__ __noinline__ void big_scales(const RowsArgs g, int row, int k0, int k
 // them, so that a row of one part has the same bits from both.  Out of line, W
 // straight from memory and steps not unrolled: the instructions of a call with
 // few rows are a good part of its time, and its common path keeps its own
-// (inlined, or sharing its code with the kernel, this cost that 5 to 13%).
-// Two parts take two to five times as long as one in the kernel.
+// (inlined, or sharing its code with the kernel, this cost that 5 to 13%; as it
+// is, within 2%).
+// Two parts take two to four times as long as one in the kernel.
 template <bool kNv, int kNg, int kWarps>
 __device__ __noinline__ void rows_in_parts(const RowsArgs g, int grp) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint32_t amax[8 * kNg];  // bits of the largest finite magnitude of each row of X
-  __shared__ int amin[8 * kNg];       // bf16 bits of the smallest that is not zero (2^16: none)
-  __shared__ int nparts;              // of the row with the most
   asm volatile("cp.async.wait_all;" ::: "memory");  // the kernel's loads ahead
+  // in the place of the rings: bits of the largest finite magnitude of each row
+  // of X, and the parts of the row with the most.  (As static arrays of this
+  // function they cost the kernel 1 to 5%: 6.5 instead of 6.3 us for
+  // 1 x 8192 x 2048.)
+  uint32_t* amax = reinterpret_cast<uint32_t*>(smem + min(g.tg, g.t) * g.xpitch);
+  int* nparts = reinterpret_cast<int*>(amax + 8 * kNg);
   float* sums = reinterpret_cast<float*>(smem + min(g.tg, g.t) * g.xpitch + kWarps * kDepth * kStepBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gr = lane >> 2, t4 = lane & 3;
@@ -335,6 +348,7 @@ __device__ __noinline__ void rows_in_parts(const RowsArgs g, int grp) {
   const int chunks = static_cast<int>(g.pitch >> 4), atoms = static_cast<int>(g.atoms);  // of a row
   int eunit = -kMxUp;
   const float unit = kNv ? significand(*g.ts, eunit) : 1.0f;
+  bool known = false;  // the ranges of X's rows
 #pragma unroll 1
   for (; grp < ngroups; grp += gridDim.x) {
     float total[kNg][4] = {};
@@ -352,8 +366,9 @@ __device__ __noinline__ void rows_in_parts(const RowsArgs g, int grp) {
 #pragma unroll 1
       do {
         __syncthreads();
-        stage_part<kNv, kNg, kWarps>(g, k0, part, t0, nt, smem, amax, amin, &nparts);
+        stage_part<kNv, kNg, kWarps>(g, k0, part, part > 0 || known, t0, nt, smem, amax, nparts);
         __syncthreads();
+        known = g.k <= g.kc;  // one pass: for the groups that follow too
         float acc[kNg][4] = {};
         uint32_t w[2][4], sw[2], next[2][4], snext[2], big = 0u;
         auto fetch = [&](int j) {
@@ -448,7 +463,7 @@ __device__ __noinline__ void rows_in_parts(const RowsArgs g, int grp) {
               total[q][i] += times_pow2(more[4 * q + i], 1.0f,
                                         exponent_of(amax[min(8 * q + 2 * t4 + (i & 1), nt - 1)], part) + kMxDown);
         }
-      } while (++part < nparts);
+      } while (++part < *nparts);
     }
     if (g.ks > 1) {
       __syncthreads();
@@ -795,10 +810,10 @@ cudaError_t launch_rows_w(const RowsArgs& g, int dev, int ctas, int smem, cudaSt
 // 19.6 us against 20.3 us as one CTA; 2048 x 8192 7.2 against 8.6 us), more
 // rows as one CTA, which copies X once (t = 16: 26.6 against 27.7 us, t = 32:
 // 39.8 against 46.1 us); eight warps where X takes the shared memory.  (These
-// were measured before rows could be taken in parts, which added 2 to 5% to
-// each; now 20.7, 7.1, 26.8, 41.4 us.)  Kernels for more than 16 rows spill 40
-// (NV) or 60 (MX) bytes, MX ones for fewer up to 12; with 24 warps of 80
-// registers the spills took t = 16 to 39.9 us.
+// pairs were measured before rows could be taken in parts; the choices made
+// now take 20.0, 6.9, 26.7 and 40.7 us.)  Kernels for more than 16 rows spill
+// 24 (NV) or 40 (MX) bytes, MX ones for fewer 8; with 24 warps of 80 registers
+// the spills took t = 16 to 39.9 us.
 template <bool kNv, int kNg>
 cudaError_t launch_rows(const RowsArgs& g, int dev, int sms, cudaStream_t st) {
   auto smem = [&](int warps) {
