@@ -94,10 +94,10 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 // Bit 7 of every byte of four e8m0 scales that is kMxBig or more.
 __device__ __forceinline__ uint32_t mx_big(uint32_t w) { return w & (w << 1) & 0x80808080u; }
 // The four scales as the exponent fields that they are taken with, kMxUp above
-// their own (a byte 0 is 2^-127, so this holds for all): plain while none is
-// big, which then counts as 0.
+// their own (a byte 0 is 2^-127, so this holds for all); none may be big, or a
+// big one counts as 0.
 __device__ __forceinline__ uint32_t mx_up(uint32_t w) { return w + kMxUp * 0x01010101u; }
-__device__ __noinline__ uint32_t mx_up_mixed(uint32_t w) {
+__device__ __forceinline__ uint32_t mx_up_mixed(uint32_t w) {
   uint32_t r = 0u;
 #pragma unroll
   for (int b = 0; b < 32; b += 8) {
@@ -267,14 +267,13 @@ __device__ __forceinline__ void store_rows(const RowsArgs& g, const float (&tota
 
 // MX: the sums of a warp's row tile (its lane's rows `row` and row + 8 of W)
 // over the blocks with big scales, times 2^-31; X of [k0, k0 + kc) is in shared
-// memory.  Rarely called, so out of line.
+// memory.
 template <int kNg>
-__device__ __noinline__ void big_scales(const RowsArgs g, int row, int k0, int ks, int nt, float* sums) {
-  extern __shared__ __align__(16) uint8_t smem[];
+__device__ __forceinline__ void big_scales(const RowsArgs& g, const uint8_t* smem, int row, int k0, int ks, int nt,
+                                           float (&acc)[kNg][4]) {
   const int lane = threadIdx.x & 31, gr = lane >> 2, t4 = lane & 3;
   const int steps = (min(g.kc, g.k - k0) + kStepK - 1) / kStepK;
   const int chunks = static_cast<int>(g.pitch >> 4), atoms = static_cast<int>(g.atoms);
-  float acc[kNg][4] = {};
 #pragma unroll 1
   for (int j = ks; j < steps; j += g.ks) {
     const int at = k0 / kStepK + j;  // step of the row, and its scale atom
@@ -313,11 +312,17 @@ __device__ __noinline__ void big_scales(const RowsArgs g, int row, int k0, int k
       }
     }
   }
-#pragma unroll
-  for (int q = 0; q < kNg; ++q)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sums[4 * q + i] = acc[q][i];
 }
+
+// What rows_in_parts works with, in shared memory in the place of the rings: as
+// an argument by value g made a stack frame, and a kernel with one takes 1 us
+// longer from stream to stream launch (28.2 instead of 26.8 us for
+// 16 x 65536 x 2048); static arrays made the common path 1 to 5% slower.
+struct PartsArgs {
+  RowsArgs g;
+  uint32_t amax[32];  // bits of the largest finite magnitude of each row of X
+  int nparts;         // of the row with the most
+};
 
 // The row tiles of a CTA from group `grp` on, for an X whose rows spread over
 // more exponents than an fp16 holds, and for big MX scales: each row tile once
@@ -329,15 +334,11 @@ __device__ __noinline__ void big_scales(const RowsArgs g, int row, int k0, int k
 // is, within 2%).
 // Two parts take two to four times as long as one in the kernel.
 template <bool kNv, int kNg, int kWarps>
-__device__ __noinline__ void rows_in_parts(const RowsArgs g, int grp) {
+__device__ __noinline__ void rows_in_parts(PartsArgs* args, int grp) {
   extern __shared__ __align__(16) uint8_t smem[];
-  asm volatile("cp.async.wait_all;" ::: "memory");  // the kernel's loads ahead
-  // in the place of the rings: bits of the largest finite magnitude of each row
-  // of X, and the parts of the row with the most.  (As static arrays of this
-  // function they cost the kernel 1 to 5%: 6.5 instead of 6.3 us for
-  // 1 x 8192 x 2048.)
-  uint32_t* amax = reinterpret_cast<uint32_t*>(smem + min(g.tg, g.t) * g.xpitch);
-  int* nparts = reinterpret_cast<int*>(amax + 8 * kNg);
+  const RowsArgs& g = args->g;
+  uint32_t* amax = args->amax;
+  int* nparts = &args->nparts;
   float* sums = reinterpret_cast<float*>(smem + min(g.tg, g.t) * g.xpitch + kWarps * kDepth * kStepBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gr = lane >> 2, t4 = lane & 3;
@@ -454,13 +455,13 @@ __device__ __noinline__ void rows_in_parts(const RowsArgs g, int grp) {
             total[q][i] += times_pow2(acc[q][i], unit, e + eunit);
           }
         if (!kNv && __any_sync(0xffffffffu, big != 0u)) {
-          float more[4 * kNg];
-          big_scales<kNg>(g, (grp * per + rw) * 16 + gr, k0, ks, nt, more);
+          float more[kNg][4] = {};
+          big_scales<kNg>(g, smem, (grp * per + rw) * 16 + gr, k0, ks, nt, more);
 #pragma unroll
           for (int q = 0; q < kNg; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              total[q][i] += times_pow2(more[4 * q + i], 1.0f,
+              total[q][i] += times_pow2(more[q][i], 1.0f,
                                         exponent_of(amax[min(8 * q + 2 * t4 + (i & 1), nt - 1)], part) + kMxDown);
         }
       } while (++part < *nparts);
@@ -486,6 +487,16 @@ __device__ __noinline__ void rows_in_parts(const RowsArgs g, int grp) {
     }
     store_rows(g, total, (grp * per + rw) * 16 + gr, t0, nt, t4);
   }
+}
+
+template <bool kNv, int kNg, int kWarps>
+__device__ __forceinline__ void call_rows_in_parts(const RowsArgs& g, uint8_t* rings, int grp) {
+  asm volatile("cp.async.wait_all;" ::: "memory");  // the loads ahead: the rings are free
+  __syncthreads();
+  PartsArgs* args = reinterpret_cast<PartsArgs*>(rings);
+  if (threadIdx.x == 0) args->g = g;
+  __syncthreads();
+  rows_in_parts<kNv, kNg, kWarps>(args, grp);
 }
 
 template <bool kNv, int kNg, int kWarps>
@@ -573,12 +584,21 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
       const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
       uint32_t a = 0u;  // two magnitudes
       least = 0x7FFF7FFFu;
-#pragma unroll 4
-      for (int p = p0; p < pieces; p += pstep) {
-        const uint4 q = piece(src, vec, p);
+      auto look = [&](const uint4& q) {
         a = __vmaxu2(__vmaxu2(a, q.x & 0x7FFF7FFFu), __vmaxu2(q.y & 0x7FFF7FFFu, __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu)));
         least = __vmins2(__vmins2(least, wrapped(q.x)), __vmins2(wrapped(q.y), __vmins2(wrapped(q.z), wrapped(q.w))));
-      }
+      };
+      int p = p0;
+      if (vec)
+        for (; (p + 7 * pstep) * 8 + 8 <= kn; p += 8 * pstep) {
+          uint4 q[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) q[u] = __ldg(reinterpret_cast<const uint4*>(src) + p + u * pstep);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) look(q[u]);
+        }
+#pragma unroll 4
+      for (; p < pieces; p += pstep) look(piece(src, vec, p));
       a = __reduce_max_sync(0xffffffffu, max(a & 0xFFFF0000u, a << 16));
       if (a >= 0x7F800000u) {  // a NaN or an infinity: the finite values alone set the power of two
         a = 0u;
@@ -625,7 +645,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
   for (int q = 0; q < kNg; ++q) xrow[q] = min(8 * q + gr, nt - 1) * g.xpitch + t4 * 16;
   const float scale_g = kNv ? *g.ts : 1.0f;
   bool staged = false;
-  uint32_t big = 0u;  // MX: scales that this kernel counts as 0 were met
+  uint32_t big = 0u;  // MX: a big scale was met, whose sums do not count
   for (int grp = blockIdx.x; grp < ngroups; grp += gridDim.x) {
     float total[kNg][4];
 #pragma unroll
@@ -646,7 +666,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
         __syncthreads();
         stage(k0);
         if (__syncthreads_or(!exact)) {
-          rows_in_parts<kNv, kNg, kWarps>(g, grp);
+          call_rows_in_parts<kNv, kNg, kWarps>(g, rings, grp);
           return;
         }
         staged = true;
@@ -690,10 +710,9 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
           }
         }
         if (!kNv) {
-          const uint32_t some = mx_big(sw[0]) | mx_big(sw[1]);
-          big |= some;
-          sw[0] = some == 0u ? mx_up(sw[0]) : mx_up_mixed(sw[0]);
-          sw[1] = some == 0u ? mx_up(sw[1]) : mx_up_mixed(sw[1]);
+          big |= mx_big(sw[0]) | mx_big(sw[1]);
+          sw[0] = mx_up(sw[0]);
+          sw[1] = mx_up(sw[1]);
         }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -788,7 +807,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) fp4_rows_kernel(cons
         else static_cast<float*>(g.out)[at] = v;
       }
   }
-  if (!kNv && __syncthreads_or(big != 0u)) rows_in_parts<kNv, kNg, kWarps>(g, blockIdx.x);  // all of them again
+  if (!kNv && __syncthreads_or(big != 0u)) call_rows_in_parts<kNv, kNg, kWarps>(g, rings, blockIdx.x);  // all of them again
 }
 
 template <bool kNv, int kNg, int kWarps>
@@ -811,9 +830,9 @@ cudaError_t launch_rows_w(const RowsArgs& g, int dev, int ctas, int smem, cudaSt
 // rows as one CTA, which copies X once (t = 16: 26.6 against 27.7 us, t = 32:
 // 39.8 against 46.1 us); eight warps where X takes the shared memory.  (These
 // pairs were measured before rows could be taken in parts; the choices made
-// now take 20.0, 6.9, 26.7 and 40.7 us.)  Kernels for more than 16 rows spill
-// 24 (NV) or 40 (MX) bytes, MX ones for fewer 8; with 24 warps of 80 registers
-// the spills took t = 16 to 39.9 us.
+// now take 20.2, 7.1, 26.1 and 40.2 us.)  Kernels for more than 16 rows spill
+// 32 (NV) or 72 (MX) bytes, MX ones for 9 to 16 rows 28; with 24 warps of 80
+// registers the spills took t = 16 to 39.9 us.
 template <bool kNv, int kNg>
 cudaError_t launch_rows(const RowsArgs& g, int dev, int sms, cudaStream_t st) {
   auto smem = [&](int warps) {
