@@ -236,3 +236,52 @@ def test_rows_product_counts_subnormals_once(fp4, fmt):
         x, x64 = bf16(x)
         got = fp4.fp4_rows_product(x, w, out_dtype=torch.float32).double().cpu().numpy()
         assert np.array_equal(got, x64 @ w64.T)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("off", [0, 1, 8])
+def test_rows_product_of_spread_rows_strided_captured_and_side_by_side(fp4, off, fmt):
+    """Rows of several parts inside larger rows, aligned and not, into strided
+    bf16 and fp32 outputs; a graph that was captured on ordinary rows replayed
+    on them; two streams at once."""
+    r = np.random.default_rng(12 + off)
+    t, n, k = 11, 333, 500
+    big = torch.zeros(t, k + 12, dtype=torch.bfloat16, device="cuda")
+    x = big[:, off:off + k]
+    x.copy_(torch.from_numpy(r.standard_normal((t, k)).astype(np.float32)))
+    codes = r.integers(0, 16, (n, k))
+    codes[::3, :k // 2] = 0
+    byte = r.integers(0, 255, (n, -(-k // 32))) // 4 + 95 if fmt == "mx" else r.integers(1, 127, (n, -(-k // 16)))
+    w, w64 = matrix(fp4, codes, byte, fmt)
+    outs = {dt: torch.full((t, n + 5), 4.0, dtype=dt, device="cuda") for dt in (torch.float32, torch.bfloat16)}
+
+    def run():
+        for out in outs.values():
+            fp4.fp4_rows_product(x, w, out=out[:, 2:n + 2])
+
+    def check():
+        for dt, out in outs.items():
+            check_rows(out[:, 2:n + 2], x.double().cpu().numpy(), w64, dt)
+            assert (out[:, :2] == 4).all() and (out[:, n + 2:] == 4).all()
+
+    run()
+    check()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    x[:, :k // 2] *= 2.0 ** 60
+    x[3] *= 2.0 ** -50
+    graph.replay()
+    torch.cuda.synchronize()
+    check()
+    want = outs[torch.float32][:, 2:n + 2].clone()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [fp4.fp4_rows_product(x, w, out_dtype=torch.float32, stream=s) for _ in range(5) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
